@@ -12,6 +12,7 @@ KREA2_OK, KREA2_ERR_ARG, KREA2_ERR_WORKSPACE, KREA2_ERR_CUDA, KREA2_ERR_TIMEOUT,
 KREA2_BF16, KREA2_F32 = 0, 1
 KREA2_EPI_STORE, KREA2_EPI_SWIGLU, KREA2_EPI_RESID = 0, 1, 2
 KREA2_NOALLOC_SCRATCH_BYTES = 64 << 20
+KREA2_MAX_REQUESTS = 4096
 
 
 class Krea2Dims(ctypes.Structure):
@@ -43,7 +44,20 @@ class Krea2TextWeights(ctypes.Structure):
                 ("layer_w", c_void_p), ("txt_in_w", c_void_p), ("txt_in_b", c_void_p)]
 
 
+class Krea2PagedBatch(ctypes.Structure):
+    _fields_ = [("R", c_int), ("M", c_int), ("q_start", c_void_p), ("kv_len", c_void_p), ("page_table", c_void_p),
+                ("max_pages", c_int), ("page_size", c_int), ("num_pages", c_int), ("k_pages", c_void_p),
+                ("v_pages", c_void_p)]
+
+
+class Krea2Lora(ctypes.Structure):
+    _fields_ = [("R", c_int), ("n_adapters", c_int), ("rank", c_int), ("row_start", c_void_p), ("adapter", c_void_p),
+                ("scale", c_void_p), ("down", c_void_p), ("up", c_void_p)]
+
+
 _PD = POINTER(Krea2Dims)
+_PPB = POINTER(Krea2PagedBatch)
+_PL = POINTER(Krea2Lora)
 _PTD = POINTER(Krea2TextDims)
 _PTW = POINTER(Krea2TextWeights)
 _PB = POINTER(Krea2BlockWeights)
@@ -84,6 +98,13 @@ SIGNATURES = {
     "krea2_gqa_attention_block_causal": (c_int, [_PD, c_int, c_int, c_int, c_int, V, V, V, V, V, V, V, V, V,
                                                  c_size_t, V]),
     "krea2_gqa_attention_noalloc": (c_int, [_PD, c_int, c_int, c_int, c_int, V, V, V, V, V, V, V, V]),
+    "krea2_paged_batch_check": (c_int, [_PPB]),
+    "krea2_paged_kv_append": (c_int, [_PD, _PPB, c_int, V, V, V, V, V]),
+    "krea2_paged_attention_workspace_size": (c_size_t, [_PD, _PPB, c_int]),
+    "krea2_gqa_attention_paged": (c_int, [_PD, _PPB, c_int, c_int, V, V, V, V, V, V, V, V, c_size_t, V]),
+    "krea2_lora_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int, c_int, c_int]),
+    "krea2_lora_linear": (c_int, [c_int, c_int, c_int, c_int, c_int, V, V, _PL, V, V, c_int, c_longlong, V, c_size_t,
+                                  V]),
 }
 
 

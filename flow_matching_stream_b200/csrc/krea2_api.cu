@@ -5,12 +5,16 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
+#include <new>
 #include <vector>
 
 #include <cuda_bf16.h>
 
+#include "krea2_device.cuh"
 #include "krea2_internal.h"
+#include "ragged.cuh"
 
 namespace krea2 {
 
@@ -291,14 +295,20 @@ const char* krea2_last_error_string(void) { return g_err; }
 int krea2_check_device_error(void* stream) {
   cudaError_t e = cudaStreamSynchronize(as_stream(stream));
   if (e != cudaSuccess) return set_error(KREA2_ERR_CUDA, "stream error: %s", cudaGetErrorString(e));
-  const int ve[2] = {take_device_error_gemm(), take_device_error_attention()};
-  const char* names[2] = {"GEMM", "attention"};
-  for (int i = 0; i < 2; ++i) {
+  constexpr int FILES = 4;
+  const int ve[FILES] = {take_device_error_gemm(), take_device_error_attention(), take_device_error_paged(),
+                         take_device_error_lora()};
+  const char* names[FILES] = {"GEMM", "attention", "paged cache", "adapter"};
+  for (int i = 0; i < FILES; ++i) {
     if (ve[i] < 0) return set_error(KREA2_ERR_CUDA, "cannot read the device error word");
-    if (ve[i] > 0)
+    if (ve[i] & ERR_WAIT_TIMEOUT)
       return set_error(KREA2_ERR_TIMEOUT, "a bounded device-side wait expired in the %s kernels (code %d)",
                        names[i], ve[i]);
   }
+  for (int i = 0; i < FILES; ++i)
+    if (ve[i] > 0)
+      return set_error(KREA2_ERR_ARG, "the %s kernels found a batch's device arrays inconsistent (row starts, lengths, "
+                       "page or adapter numbers)", names[i]);
   return KREA2_OK;
 }
 
@@ -787,6 +797,144 @@ int krea2_backbone_forward(const Krea2Dims* dims, int B, int T, int N, int dtype
     if ((rc = block_impl(dims, B, T, N, dtype, h, temb, &w->blocks[l], cs, sn, mask, ws, L, s))) return rc;
   // the block activations are dead now: their bf16 xn buffer (B*S*C) holds the final norm's output
   return final_layer_impl(dims, B, T, N, bf, h, e, w, velocity, ws + L.xn, s);
+}
+
+namespace {
+// Sizes and pointers of a paged batch that every entry point needs (the device arrays' contents are
+// checked by the kernels, or on the host by krea2_paged_batch_check).
+int check_batch_sizes(const Krea2PagedBatch* b) {
+  if (!b) return set_error(KREA2_ERR_ARG, "batch is NULL");
+  if (b->R < 1 || b->M < 1 || b->M > (1 << 30)) return set_error(KREA2_ERR_ARG, "need R >= 1 and 1 <= M <= 2^30");
+  if (b->R > KREA2_MAX_REQUESTS)
+    return set_error(KREA2_ERR_UNSUPPORTED, "%d requests, at most %d", b->R, (int)KREA2_MAX_REQUESTS);
+  if (b->max_pages < 1 || b->num_pages < 1 || b->page_size < 1)
+    return set_error(KREA2_ERR_ARG, "max_pages, num_pages and page_size must be positive");
+  if ((long long)b->max_pages * b->page_size > (1LL << 30))
+    return set_error(KREA2_ERR_ARG, "max_pages * page_size exceeds 2^30");
+  if (b->page_size % 16) return set_error(KREA2_ERR_UNSUPPORTED, "page_size must be a multiple of 16");
+  return KREA2_OK;
+}
+
+int check_batch(const Krea2PagedBatch* b) {
+  int rc = check_batch_sizes(b);
+  if (rc) return rc;
+  if (!b->q_start || !b->kv_len || !b->page_table || !b->k_pages || !b->v_pages)
+    return set_error(KREA2_ERR_ARG, "batch: NULL pointer");
+  if ((reinterpret_cast<uintptr_t>(b->k_pages) | reinterpret_cast<uintptr_t>(b->v_pages)) & 15)
+    return set_error(KREA2_ERR_ARG, "k_pages and v_pages must be 16-byte aligned");
+  return KREA2_OK;
+}
+}  // namespace
+
+int krea2_paged_batch_check(const Krea2PagedBatch* b) {
+  int rc = check_batch_sizes(b);
+  if (rc) return rc;
+  if (!b->q_start || !b->kv_len || !b->page_table) return set_error(KREA2_ERR_ARG, "batch: NULL pointer");
+  const long long capacity = (long long)b->max_pages * b->page_size;
+  try {
+    std::vector<long long> slots;  // pool rows that receive a new token
+    for (int r = 0; r < b->R; ++r) {
+      RequestRows q;
+      if (!request_rows(r, b->M, capacity, b->q_start, b->kv_len, &q))
+        return set_error(KREA2_ERR_ARG, "request %d: rows [%d, %d) of %d, %d keys of at most %lld", r, q.row0,
+                         b->q_start[r + 1], b->M, q.L, capacity);
+      const int32_t* pages = b->page_table + (long long)r * b->max_pages;
+      for (int i = 0; q.n > 0 && i < (q.L + b->page_size - 1) / b->page_size; ++i)
+        if (pages[i] < 0 || pages[i] >= b->num_pages)
+          return set_error(KREA2_ERR_ARG, "request %d: page %d has number %d, the pool has %d pages", r, i, pages[i],
+                           b->num_pages);
+      for (int t = q.L - q.n; t < q.L; ++t)
+        slots.push_back((long long)pages[t / b->page_size] * b->page_size + t % b->page_size);
+    }
+    std::sort(slots.begin(), slots.end());
+    const auto twice = std::adjacent_find(slots.begin(), slots.end());
+    if (twice != slots.end())
+      return set_error(KREA2_ERR_ARG, "two new tokens have slot %lld of page %lld", *twice % b->page_size,
+                       *twice / b->page_size);
+  } catch (const std::bad_alloc&) {
+    return set_error(KREA2_ERR_UNSUPPORTED, "no host memory to check the batch's slots");
+  }
+  return KREA2_OK;
+}
+
+int krea2_paged_kv_append(const Krea2Dims* dims, const Krea2PagedBatch* batch, int dtype, const void* qkvg,
+                          const float* k_norm_w, const float* cos, const float* sin, void* stream) {
+  int rc = check_dims(dims, dtype);
+  if (rc || (rc = check_batch(batch))) return rc;
+  if (!qkvg || !k_norm_w || !cos || !sin) return set_error(KREA2_ERR_ARG, "NULL pointer");
+  if (reinterpret_cast<uintptr_t>(qkvg) & 15) return set_error(KREA2_ERR_ARG, "qkvg must be 16-byte aligned");
+  return launch_paged_append(*batch, dims, dtype == KREA2_BF16, qkvg, k_norm_w, cos, sin, as_stream(stream));
+}
+
+size_t krea2_paged_attention_workspace_size(const Krea2Dims* dims, const Krea2PagedBatch* batch, int dtype) {
+  if (check_dims(dims, dtype) || check_batch_sizes(batch)) return 0;
+  return 0;
+}
+
+int krea2_gqa_attention_paged(const Krea2Dims* dims, const Krea2PagedBatch* batch, int T, int dtype, const void* qkvg,
+                              const float* q_norm_w, const float* cos, const float* sin, const uint8_t* text_mask,
+                              const int32_t* key_end, void* out, void* workspace, size_t ws_bytes, void* stream) {
+  int rc = check_dims(dims, dtype);
+  if (rc || (rc = check_batch(batch))) return rc;
+  if (T < 0) return set_error(KREA2_ERR_ARG, "text length must be >= 0");
+  if (!qkvg || !q_norm_w || !cos || !sin || !out) return set_error(KREA2_ERR_ARG, "NULL pointer");
+  if ((reinterpret_cast<uintptr_t>(qkvg) | reinterpret_cast<uintptr_t>(out)) & 15)
+    return set_error(KREA2_ERR_ARG, "qkvg and out must be 16-byte aligned");
+  const size_t need = krea2_paged_attention_workspace_size(dims, batch, dtype);
+  if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255)))
+    return set_error(KREA2_ERR_WORKSPACE, "workspace must be non-NULL and 256-byte aligned");
+  if (ws_bytes < need) return set_error(KREA2_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+  PagedAttnArgs a{};
+  a.H = dims->H; a.Hkv = dims->Hkv; a.T = T; a.eps = dims->eps;
+  a.scale_log2 = 1.4426950408889634f / sqrtf((float)dims->D);
+  a.qkvg = qkvg; a.q_norm_w = q_norm_w; a.cos = cos; a.sin = sin;
+  a.text_mask = T > 0 ? text_mask : nullptr; a.key_end = key_end;
+  a.k_pages = batch->k_pages; a.v_pages = batch->v_pages; a.out = out;
+  return launch_paged_attn_simt(*batch, a, dims->D, dtype == KREA2_BF16, as_stream(stream));
+}
+
+namespace {
+int check_lora_sizes(int dtype, int epilogue, int M, int Nw, int K, int R, int rank) {
+  if (dtype != KREA2_BF16 && dtype != KREA2_F32) return set_error(KREA2_ERR_ARG, "unknown dtype %d", dtype);
+  if (epilogue < EPI_STORE || epilogue > EPI_RESID) return set_error(KREA2_ERR_ARG, "unknown epilogue %d", epilogue);
+  if (M <= 0 || Nw <= 0 || K <= 0 || R <= 0) return set_error(KREA2_ERR_ARG, "sizes must be positive");
+  if (M > (1 << 22)) return set_error(KREA2_ERR_UNSUPPORTED, "at most 2^22 rows");
+  if (R > KREA2_MAX_REQUESTS) return set_error(KREA2_ERR_UNSUPPORTED, "%d requests, at most %d", R, (int)KREA2_MAX_REQUESTS);
+  if (rank < 8 || rank > 256 || rank % 8) return set_error(KREA2_ERR_UNSUPPORTED, "rank must be a multiple of 8, 8..256");
+  if (epilogue == EPI_SWIGLU && Nw % 128) return set_error(KREA2_ERR_ARG, "SwiGLU needs Nw %% 128 == 0");
+  if (dtype == KREA2_BF16 && (Nw % 128 || K % 64))
+    return set_error(KREA2_ERR_UNSUPPORTED, "bf16 linear needs Nw %% 128 == 0 and K %% 64 == 0");
+  return KREA2_OK;
+}
+}  // namespace
+
+size_t krea2_lora_workspace_size(int dtype, int epilogue, int M, int Nw, int K, int R, int rank) {
+  if (check_lora_sizes(dtype, epilogue, M, Nw, K, R, rank)) return 0;
+  return lora_workspace_bytes(dtype, epilogue, M, Nw, K, R, rank);
+}
+
+int krea2_lora_linear(int dtype, int epilogue, int M, int Nw, int K, const void* A, const void* W, const Krea2Lora* lora,
+                      void* out, const float* gate, int rows_per_batch, long long gate_stride, void* workspace,
+                      size_t ws_bytes, void* stream) {
+  if (!lora) return set_error(KREA2_ERR_ARG, "lora is NULL");
+  int rc = check_lora_sizes(dtype, epilogue, M, Nw, K, lora->R, lora->rank);
+  if (rc) return rc;
+  if (!A || !W || !out || !lora->row_start || !lora->adapter) return set_error(KREA2_ERR_ARG, "NULL pointer");
+  if (lora->n_adapters < 1 || !lora->scale || !lora->down || !lora->up)
+    return set_error(KREA2_ERR_ARG, "need n_adapters >= 1 and scale, down and up");
+  if (epilogue == EPI_RESID && (!gate || rows_per_batch < 0 || gate_stride < 0))
+    return set_error(KREA2_ERR_ARG, "residual epilogue needs gate, rows_per_batch >= 0, gate_stride >= 0");
+  if ((reinterpret_cast<uintptr_t>(A) | reinterpret_cast<uintptr_t>(W) | reinterpret_cast<uintptr_t>(out) |
+       reinterpret_cast<uintptr_t>(lora->down) | reinterpret_cast<uintptr_t>(lora->up)) & 15)
+    return set_error(KREA2_ERR_ARG, "A, W, down, up and out must be 16-byte aligned");
+  const size_t need = lora_workspace_bytes(dtype, epilogue, M, Nw, K, lora->R, lora->rank);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return set_error(KREA2_ERR_WORKSPACE, "workspace must be non-NULL and 256-byte aligned");
+  if (ws_bytes < need) return set_error(KREA2_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+  LoraLinearArgs a{};
+  a.M = M; a.N = Nw; a.K = K; a.A = A; a.W = W; a.out = out;
+  a.gate = gate; a.rows_per_batch = rows_per_batch; a.gate_stride = gate_stride;
+  return launch_lora_linear(dtype, epilogue, a, *lora, workspace, as_stream(stream));
 }
 
 }  // extern "C"

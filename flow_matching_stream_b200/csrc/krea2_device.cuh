@@ -26,6 +26,7 @@ static __device__ int g_device_error = 0;
   }
 
 constexpr int ERR_WAIT_TIMEOUT = 1;
+constexpr int ERR_BAD_BATCH = 2;  // a ragged batch's device arrays are inconsistent
 // A single barrier wait never legitimately lasts this long (kernels take milliseconds).
 constexpr unsigned long long WAIT_LIMIT_NS = 2000000000ull;  // 2 s
 

@@ -29,6 +29,8 @@ void count_launch();
 // Read and clear the device error word of the GEMM / attention files (0 = none, -1 = read failed).
 int take_device_error_gemm();
 int take_device_error_attention();
+int take_device_error_paged();
+int take_device_error_lora();
 
 struct GemmParams {
   int M, N, K;              // N = rows of W
@@ -151,5 +153,35 @@ int launch_kv_append(const void* qkvg, long long stride, int B, int n, int H, in
 // raw [q | k] -> normalised + rotated [q | k] (bf16, row stride (H+Hkv)*128)
 int launch_qk_prep(const void* qkvg, long long stride, int B, int S, int H, int Hkv, float eps, const float* qw,
                    const float* kw, const float* cs, const float* sn, void* dst, cudaStream_t stream);
+
+// Ragged batches (paged_simt.cu, lora.cu).
+struct PagedAttnArgs {
+  int H, Hkv, T;
+  float eps, scale_log2;  // log2(e) / sqrt(D)
+  const void* qkvg;       // (M, 2*H*D + 2*Hkv*D)
+  const float* q_norm_w;
+  const float* cos;       // (M, D/2)
+  const float* sin;
+  const uint8_t* text_mask;  // (R, T) or null
+  const int32_t* key_end;    // (M) or null
+  const void* k_pages;
+  const void* v_pages;
+  void* out;              // (M, H*D)
+};
+int launch_paged_append(const Krea2PagedBatch& b, const Krea2Dims* d, bool bf16, const void* qkvg, const float* kw,
+                        const float* cs, const float* sn, cudaStream_t stream);
+int launch_paged_attn_simt(const Krea2PagedBatch& b, const PagedAttnArgs& a, int D, bool bf16, cudaStream_t stream);
+
+struct LoraLinearArgs {
+  int M, N, K;
+  const void* A;
+  const void* W;
+  void* out;
+  const float* gate;
+  int rows_per_batch;     // RESID: 0 takes the gate row of the row's request
+  long long gate_stride;
+};
+size_t lora_workspace_bytes(int dtype, int epi, int M, int N, int K, int R, int rank);
+int launch_lora_linear(int dtype, int epi, const LoraLinearArgs& a, const Krea2Lora& l, void* ws, cudaStream_t stream);
 
 }  // namespace krea2

@@ -24,6 +24,8 @@ __all__ = [
     "text_dims_struct", "TextWeights", "text_fusion_workspace_size", "text_fusion",
     "shift_mu", "sigma_schedule", "euler_cfg_step", "sample_workspace_size", "sample",
     "block_forward", "block_forward_traced", "BLOCK_STEPS", "launch_count", "backbone_forward", "check_device_error", "BlockWeights", "ModelWeights",
+    "PagedBatch", "paged_batch_check", "paged_kv_append", "paged_attention_workspace_size", "gqa_attention_paged",
+    "LoraAdapters", "lora_workspace_size", "lora_linear",
     "interleave_gate_up", "KREA2_BF16", "KREA2_F32", "KREA2_EPI_STORE", "KREA2_EPI_SWIGLU", "KREA2_EPI_RESID",
 ]
 
@@ -49,7 +51,11 @@ def _check(rc: int) -> None:
 
 
 def dims_struct(d) -> _lib.Krea2Dims:
-    """Krea2Dims from any object with C, H, Hkv, D, F, axes, theta, eps, n_layers, in_ch, t_dim."""
+    """Krea2Dims from any object with C, H, Hkv, D, F, axes, theta, eps, n_layers, in_ch, t_dim.
+
+    A Krea2Dims is returned as it is, so a caller of many short calls can build it once."""
+    if isinstance(d, _lib.Krea2Dims):
+        return d
     s = _lib.Krea2Dims()
     s.C, s.H, s.Hkv, s.D, s.F = d.C, d.H, d.Hkv, d.D, d.F
     s.axes[0], s.axes[1], s.axes[2] = tuple(d.axes)
@@ -315,6 +321,205 @@ def backbone_forward(dims, B: int, T: int, N: int, hidden_states: torch.Tensor, 
                                         _p(text_states), _p(position_ids), _p(text_mask), _p(timestep),
                                         ctypes.byref(mw.struct), _p(velocity), _p(workspace),
                                         workspace.numel() * workspace.element_size(), _s(stream)))
+
+
+# ----------------------------------------------------------------------------- ragged batches
+
+def _on(device: torch.device, stream, *tensors: Optional[torch.Tensor]) -> int:
+    """The stream to launch on, once every tensor and the stream are known to be on the current device."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"expected all tensors on {device}, got one on {t.device}")
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    elif stream.device != device:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
+    return stream.cuda_stream
+
+
+def _shape(t: torch.Tensor, shape: tuple, name: str) -> None:
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+
+
+class PagedBatch:
+    """A ragged batch over a paged key/value cache: device tensors plus the Krea2PagedBatch struct.
+
+    q_start (R + 1), kv_len (R), page_table (R, max_pages): int32; k_pages, v_pages (num_pages, page_size,
+    Hkv*D); rows: the packed rows that qkvg and out have (at least q_start[R]). The lengths and page
+    numbers stay on the device and may change between calls, under a captured graph too."""
+
+    def __init__(self, q_start: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor, k_pages: torch.Tensor,
+                 v_pages: torch.Tensor, rows: int):
+        for t, n in ((q_start, "q_start"), (kv_len, "kv_len"), (page_table, "page_table")):
+            _want(t, torch.int32, n)
+        if kv_len.dim() != 1 or page_table.dim() != 2:
+            raise ValueError("kv_len must be (R), page_table (R, max_pages)")
+        R = kv_len.shape[0]
+        _shape(q_start, (R + 1,), "q_start")
+        _shape(page_table, (R, page_table.shape[1]), "page_table")
+        if k_pages.dim() != 3 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
+            raise ValueError("k_pages and v_pages must both be (num_pages, page_size, Hkv*D) of one dtype")
+        self.dtype, self.device = k_pages.dtype, k_pages.device
+        self.tensors = (q_start, kv_len, page_table, k_pages, v_pages)
+        s = _lib.Krea2PagedBatch()
+        s.R, s.M, s.max_pages = R, rows, page_table.shape[1]
+        s.num_pages, s.page_size = k_pages.shape[0], k_pages.shape[1]
+        s.q_start, s.kv_len, s.page_table, s.k_pages, s.v_pages = (_p(t) for t in self.tensors)
+        if any(t.device != self.device for t in self.tensors):
+            raise ValueError("the batch's tensors must be on one device")
+        self.rows, self.kv_cols = rows, k_pages.shape[2]
+        self.struct = s
+
+
+def paged_batch_check(q_start, kv_len, page_table, num_pages: int, page_size: int, rows: int) -> None:
+    """Checks a batch's lengths and page numbers on the host (arrays or CPU tensors)."""
+    host = [np.ascontiguousarray(a, dtype=np.int32) for a in (q_start, kv_len, page_table)]
+    R = host[1].shape[0]
+    if host[0].shape != (R + 1,) or host[2].ndim != 2 or host[2].shape[0] != R:
+        raise ValueError("need q_start (R + 1), kv_len (R) and page_table (R, max_pages)")
+    s = _lib.Krea2PagedBatch()
+    s.R, s.M, s.max_pages, s.page_size, s.num_pages = R, rows, host[2].shape[1], page_size, num_pages
+    s.q_start, s.kv_len, s.page_table = (a.ctypes.data for a in host)
+    _check(lib().krea2_paged_batch_check(ctypes.byref(s)))
+
+
+def _paged_args(d: _lib.Krea2Dims, batch: PagedBatch, qkvg: torch.Tensor, norm_w: torch.Tensor, cos: torch.Tensor,
+                sin: torch.Tensor) -> None:
+    if batch.dtype != qkvg.dtype:
+        raise TypeError(f"the pages are {batch.dtype}, qkvg is {qkvg.dtype}")
+    if batch.kv_cols != d.Hkv * d.D:
+        raise ValueError(f"the pages have {batch.kv_cols} columns, the model has Hkv*D = {d.Hkv * d.D}")
+    _shape(qkvg, (batch.rows, 2 * (d.H + d.Hkv) * d.D), "qkvg")
+    for t, n in ((norm_w, "norm weight"), (cos, "cos"), (sin, "sin")):
+        _want(t, torch.float32, n)
+    _shape(norm_w, (d.D,), "norm weight")
+    _shape(cos, (batch.rows, d.D // 2), "cos")
+    _shape(sin, (batch.rows, d.D // 2), "sin")
+
+
+def paged_kv_append(dims, batch: PagedBatch, qkvg: torch.Tensor, k_norm_w: torch.Tensor, cos: torch.Tensor,
+                    sin: torch.Tensor, stream=None) -> None:
+    """Keys and values of a ragged batch's new tokens into its pages."""
+    d = dims_struct(dims)
+    _paged_args(d, batch, qkvg, k_norm_w, cos, sin)
+    st = _on(batch.device, stream, qkvg, k_norm_w, cos, sin)
+    _check(lib().krea2_paged_kv_append(ctypes.byref(d), ctypes.byref(batch.struct), dtype_code(qkvg.dtype), _p(qkvg),
+                                       _p(k_norm_w), _p(cos), _p(sin), st))
+
+
+def paged_attention_workspace_size(dims, batch: PagedBatch, dtype: torch.dtype) -> int:
+    return int(lib().krea2_paged_attention_workspace_size(ctypes.byref(dims_struct(dims)), ctypes.byref(batch.struct),
+                                                          dtype_code(dtype)))
+
+
+def gqa_attention_paged(dims, batch: PagedBatch, qkvg: torch.Tensor, q_norm_w: torch.Tensor, cos: torch.Tensor,
+                        sin: torch.Tensor, text_mask: Optional[torch.Tensor], key_end: Optional[torch.Tensor],
+                        out: torch.Tensor, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Attention of a ragged batch's new tokens over its pages; text_mask (R, T) uint8, key_end (rows) int32."""
+    d = dims_struct(dims)
+    _paged_args(d, batch, qkvg, q_norm_w, cos, sin)
+    _want(out, qkvg.dtype, "out")
+    _shape(out, (batch.rows, d.H * d.D), "out")
+    T = 0
+    if text_mask is not None:
+        _want(text_mask, torch.uint8, "text_mask")
+        T = text_mask.shape[-1]
+        _shape(text_mask, (batch.struct.R, T), "text_mask")
+    if key_end is not None:
+        _want(key_end, torch.int32, "key_end")
+        _shape(key_end, (batch.rows,), "key_end")
+    st = _on(batch.device, stream, qkvg, q_norm_w, cos, sin, text_mask, key_end, out, workspace)
+    ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().krea2_gqa_attention_paged(ctypes.byref(d), ctypes.byref(batch.struct), T, dtype_code(qkvg.dtype),
+                                           _p(qkvg), _p(q_norm_w), _p(cos), _p(sin), _p(text_mask), _p(key_end),
+                                           _p(out), _p(workspace), ws, st))
+
+
+class LoraAdapters:
+    """Low-rank adapters of one projection: down (n, rank, K), up (n, Nw, rank) in the projection's dtype, scale
+    (n) fp32. `up` has the order of the projection's weight rows (interleave_gate_up for SwiGLU)."""
+
+    def __init__(self, down: torch.Tensor, up: torch.Tensor, scale: torch.Tensor):
+        if down.dim() != 3 or up.dim() != 3 or up.dtype != down.dtype:
+            raise ValueError("need down (n, rank, K) and up (n, Nw, rank) of one dtype")
+        n, self.rank, self.K = down.shape
+        self.Nw = up.shape[1]
+        _shape(up, (n, self.Nw, self.rank), "up")
+        _want(scale, torch.float32, "scale")
+        _shape(scale, (n,), "scale")
+        self.down, self.up, self.scale = down, up, scale
+        self.dtype, self.device = down.dtype, down.device
+        if up.device != self.device or scale.device != self.device:
+            raise ValueError("the adapters' tensors must be on one device")
+        self.struct = _lib.Krea2Lora()
+        self.struct.n_adapters, self.struct.rank = n, self.rank
+        self.struct.down, self.struct.up, self.struct.scale = _p(down), _p(up), _p(scale)
+
+    @staticmethod
+    def fused(parts: Sequence[Sequence[tuple]], scale: torch.Tensor) -> "LoraAdapters":
+        """Adapters of stacked projections (to_q, to_k, to_v, to_gate of w_qkvg) from those of each one.
+
+        parts[a] lists adapter a's (down (r, K), up (N_i, r)) per projection, in the order of the stacked
+        rows. Ranks add up (padded to a multiple of 8), and `up` is block diagonal."""
+        rank = max(sum(d.shape[0] for d, _ in p) for p in parts)
+        rank = max(8, (rank + 7) // 8 * 8)
+        d0 = parts[0][0][0]
+        down = d0.new_zeros(len(parts), rank, d0.shape[1])
+        up = d0.new_zeros(len(parts), sum(u.shape[0] for _, u in parts[0]), rank)
+        for a, p in enumerate(parts):
+            j = c = 0
+            for d, u in p:
+                down[a, j:j + d.shape[0]] = d
+                up[a, c:c + u.shape[0], j:j + d.shape[0]] = u
+                j, c = j + d.shape[0], c + u.shape[0]
+        return LoraAdapters(down, up, scale)
+
+
+def lora_workspace_size(dtype: torch.dtype, epilogue: int, M: int, Nw: int, K: int, R: int, rank: int) -> int:
+    return int(lib().krea2_lora_workspace_size(dtype_code(dtype), epilogue, M, Nw, K, R, rank))
+
+
+def lora_linear(epilogue: int, A: torch.Tensor, W: torch.Tensor, adapters: LoraAdapters, row_start: torch.Tensor,
+                adapter: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor, gate: Optional[torch.Tensor] = None,
+                rows_per_batch: int = 0, gate_stride: Optional[int] = None, stream=None) -> None:
+    """linear() with the adapter of each row's request; row_start (R + 1) and adapter (R) int32 device tensors.
+
+    rows_per_batch = 0 gates a residual with the gate row of the row's request; gate_stride None is the
+    gate's row length."""
+    M, K = A.shape
+    Nw = W.shape[0]
+    if W.shape[1] != K:
+        raise ValueError("A and W disagree on K")
+    _want(W, A.dtype, "W")
+    _want(adapters.down, A.dtype, "adapters")
+    if adapters.K != K or adapters.Nw != Nw:
+        raise ValueError(f"adapters are for a ({adapters.Nw}, {adapters.K}) projection, W is ({Nw}, {K})")
+    _want(row_start, torch.int32, "row_start")
+    _want(adapter, torch.int32, "adapter")
+    R = adapter.shape[0]
+    _shape(row_start, (R + 1,), "row_start")
+    _shape(adapter, (R,), "adapter")
+    resid = epilogue == KREA2_EPI_RESID
+    _want(out, torch.float32 if resid else A.dtype, "out")
+    _shape(out, (M, Nw // 2 if epilogue == KREA2_EPI_SWIGLU else Nw), "out")
+    if resid:
+        if gate is None:
+            raise ValueError("a residual epilogue needs a gate")
+        _want(gate, torch.float32, "gate")
+        if gate_stride is None:
+            gate_stride = gate.shape[-1]
+        rows = R if rows_per_batch == 0 else (M + rows_per_batch - 1) // max(rows_per_batch, 1)
+        if gate.numel() < (rows - 1) * gate_stride + Nw:
+            raise ValueError(f"the gate has {gate.numel()} values, {rows} rows of stride {gate_stride} are read")
+    st = _on(A.device, stream, W, adapters.down, row_start, adapter, out, workspace, gate)
+    s = _lib.Krea2Lora.from_buffer_copy(adapters.struct)
+    s.R, s.row_start, s.adapter = R, _p(row_start), _p(adapter)
+    _check(lib().krea2_lora_linear(dtype_code(A.dtype), epilogue, M, Nw, K, _p(A), _p(W), ctypes.byref(s), _p(out),
+                                   _p(gate), rows_per_batch, gate_stride or 0, _p(workspace),
+                                   workspace.numel() * workspace.element_size(), st))
 
 
 # ----------------------------------------------------------------------------- weights

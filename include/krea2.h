@@ -401,6 +401,108 @@ int krea2_backbone_forward(const Krea2Dims* dims, int B, int T, int N, int dtype
                            const float* timestep, const Krea2ModelWeights* w,
                            void* velocity, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---- serving a ragged batch of requests -------------------------------------------------------
+ * Several requests in one batch: new tokens packed row after row, every request with its own number
+ * of new tokens, its own cached length and its own adapter. The lengths are DEVICE arrays, so one
+ * captured CUDA graph serves batches of changing lengths.
+ *
+ * Keys and values live in pages: k_pages and v_pages are pools of num_pages pages of page_size
+ * tokens, and request r's token at position t is row t % page_size of page
+ * page_table[r * max_pages + t / page_size].
+ *   R          requests, 1..KREA2_MAX_REQUESTS
+ *   M          packed rows that qkvg and out have, 1..2^30; rows from q_start[R] on belong to no
+ *              request and are neither read nor written
+ *   q_start    (R + 1) int32: request r's new tokens are rows [q_start[r], q_start[r + 1]); q_start[0]
+ *              is 0. A request may have no new token.
+ *   kv_len     (R) int32: keys of request r, its new tokens included (they are its last keys)
+ *   page_table (R, max_pages) int32; entries past a request's last page are not read. Requests may
+ *              share pages that they only read (a common prefix).
+ *   page_size  a multiple of 16; max_pages * page_size <= 2^30
+ *   k_pages, v_pages (num_pages, page_size, Hkv*D) in `dtype`, 16-byte aligned
+ * A request whose lengths are inconsistent (q_start not ascending or beyond M, kv_len below its new
+ * tokens or beyond max_pages * page_size) is skipped: its rows and pages stay as they were. A page
+ * number outside [0, num_pages) is never accessed; output rows that needed it are unspecified. Both
+ * set the device error word, which krea2_check_device_error reports as KREA2_ERR_ARG. */
+enum { KREA2_MAX_REQUESTS = 4096 };
+typedef struct {
+  int R, M;
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const int32_t* page_table;
+  int max_pages, page_size, num_pages;
+  void* k_pages;
+  void* v_pages;
+} Krea2PagedBatch;
+
+/* Checks a batch on the host: q_start, kv_len and page_table are HOST arrays here, and k_pages and
+ * v_pages are not looked at. KREA2_ERR_ARG names the first request that is inconsistent, has a page
+ * number outside [0, num_pages), or appends to a token slot that another new token also has. */
+int krea2_paged_batch_check(const Krea2PagedBatch* batch);
+
+/* krea2_kv_cache_append for a paged batch: the keys and values of all new tokens into their pages.
+ *   qkvg (M, H*D + 2*Hkv*D + H*D) raw fused projection of the new tokens; only k and v columns are
+ *   read. cos, sin (M, D/2) fp32: RoPE tables of the packed rows.
+ * bf16 and fp32, D in {64, 128}. No two new tokens may have the same slot. */
+int krea2_paged_kv_append(const Krea2Dims* dims, const Krea2PagedBatch* batch, int dtype,
+                          const void* qkvg, const float* k_norm_w, const float* cos, const float* sin,
+                          void* stream);
+
+/* krea2_gqa_attention_kv_cache for a paged batch: the new tokens of every request over the request's
+ * kv_len keys, which must already be in the pages (krea2_paged_kv_append).
+ *   text_mask (R, T) uint8 (NULL: all valid): removes padded keys among the request's first T.
+ *   key_end NULL: every new token reads all kv_len keys. key_end (M) int32 DEVICE: row i reads keys
+ *     [0, key_end[i]) (positions in its request); a value below the token's own position + 1 is
+ *     raised to it, one above kv_len is cut to it.
+ *   qkvg, cos, sin as in krea2_paged_kv_append; q and gate columns are read.
+ *   out (M, H*D) in `dtype`: sigmoid(gate) * attention, heads merged. A token with no readable key
+ *     outputs zeros.
+ * Keys past kv_len and keys that text_mask removes are not used, whatever their pages hold (NaN
+ * included). A key that key_end hides from one token of a request but not from all must be finite.
+ *   workspace: krea2_paged_attention_workspace_size bytes, 256-byte aligned (NULL allowed when that
+ *     is 0). It needs no initial value; calls that may overlap on the GPU need one each.
+ * Kernels: bf16 with D = 128 and H/Hkv in {1, 2, 4} runs on the tensor cores; other shapes and fp32
+ * run a SIMT kernel (D in {64, 128}). */
+size_t krea2_paged_attention_workspace_size(const Krea2Dims* dims, const Krea2PagedBatch* batch, int dtype);
+int krea2_gqa_attention_paged(const Krea2Dims* dims, const Krea2PagedBatch* batch, int T, int dtype,
+                              const void* qkvg, const float* q_norm_w, const float* cos, const float* sin,
+                              const uint8_t* text_mask, const int32_t* key_end, void* out,
+                              void* workspace, size_t ws_bytes, void* stream);
+
+/* Low-rank adapters of R requests beside a shared projection.
+ *   row_start (R + 1) int32 DEVICE: request r has rows [row_start[r], row_start[r + 1]) of A;
+ *             row_start[0] is 0. Rows from row_start[R] on are neither read nor written.
+ *   adapter   (R) int32 DEVICE: the request's adapter in [0, n_adapters), or -1 for none
+ *   scale     (n_adapters) fp32
+ *   down      (n_adapters, rank, K) in `dtype`
+ *   up        (n_adapters, Nw, rank) in `dtype`, rows in the order of W's rows (for KREA2_EPI_SWIGLU
+ *             gate and up rows interleaved in 64-row groups, for a fused projection stacked)
+ *   rank      a multiple of 8, 8..256 (adapters of lower rank are padded with zeros)
+ * row_start that does not ascend from 0 to at most M, or an adapter number outside [-1, n_adapters),
+ * sets the device error word (KREA2_ERR_ARG from krea2_check_device_error); the rows concerned are
+ * then unspecified, and nothing outside the arrays is accessed. */
+typedef struct {
+  int R, n_adapters, rank;
+  const int32_t* row_start;
+  const int32_t* adapter;
+  const float* scale;
+  const void* down;
+  const void* up;
+} Krea2Lora;
+
+/* krea2_linear with the adapters' part added before the epilogue: with a = adapter[request of row],
+ *   y = A · Wᵀ + scale[a] (A · down[a]ᵀ) · up[a]ᵀ        (a = -1: y = A · Wᵀ),
+ * then the epilogue of krea2_linear on y. The inner product A · down[a]ᵀ is kept to at least 16 bits
+ * of mantissa (bf16) or in fp32.
+ * KREA2_EPI_RESID: rows_per_batch > 0 takes the gate row r / rows_per_batch as krea2_linear does;
+ * rows_per_batch = 0 takes the gate row of the row's request.
+ * bf16 path: Nw % 128 == 0, K % 64 == 0; A, W, down, up and out 16-byte aligned.
+ * workspace: krea2_lora_workspace_size bytes, 256-byte aligned; it needs no initial value, and calls
+ * that may overlap on the GPU need one each. */
+size_t krea2_lora_workspace_size(int dtype, int epilogue, int M, int Nw, int K, int R, int rank);
+int krea2_lora_linear(int dtype, int epilogue, int M, int Nw, int K, const void* A, const void* W,
+                      const Krea2Lora* lora, void* out, const float* gate, int rows_per_batch,
+                      long long gate_stride, void* workspace, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
