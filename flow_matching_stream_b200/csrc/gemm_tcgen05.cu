@@ -19,6 +19,10 @@
 //               shared-memory boxes that TMA stores; the fp32 residual and the row-mapped
 //               output pass through a padded shared tile so that global accesses run in whole
 //               128-byte row segments.
+// With low-rank adapters (LORA) a tile's K steps go on past K: for each request with an adapter among
+// the tile's rows, steps whose A operand is the request's low-rank product t (rows of other requests
+// are zero) and whose W operand is the adapter's up matrix, into the same accumulator. lora_tc.cu
+// says how t is laid out. The row count is then read on the device.
 // Tiles are visited in raster groups of row tiles, sized so that one wave of tiles reads about
 // as many A bytes as W bytes per K step and so that concurrently running CTAs share A and W
 // tiles through L2.
@@ -30,6 +34,8 @@
 
 #include "krea2_device.cuh"
 #include "krea2_internal.h"
+#include "lora.cuh"
+#include "ragged.cuh"
 
 namespace krea2 {
 
@@ -54,7 +60,7 @@ struct GemmCfg {
   static constexpr int A_BYTES = BM * BK * 2;   // 16 KB
   static constexpr int B_BYTES = BN * BK * 2;   // 32 KB (BN=256) or 16 KB (BN=128)
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = (BN == 256) ? 4 : 6;
+  static constexpr int STAGES = (BN == 256) ? 4 : (BN == 128) ? 6 : 8;
   // Epilogue staging per warp: two 4 KB swizzled 32x64 bf16 boxes (TMA-store epilogues), or one
   // padded 32x33 fp32 tile (residual and row-mapped epilogues), at 8 KB spacing.
   static constexpr int EPI_WARP_BYTES = 8192;
@@ -112,10 +118,26 @@ __device__ __forceinline__ void store_box_bf16(uint8_t* box, const uint32_t* pk,
   }
 }
 
-template <int BN, int EPI>
-__global__ void __launch_bounds__(gemm_threads<EPI>(), 1)
-    gemm_bf16_tcgen05_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                             const __grid_constant__ CUtensorMap tmC, GemmParams p) {
+// A row of a 32 x 64 bf16 block straight to global memory (the block that the last request's last row
+// cuts: a TMA store would write the rows behind it too).
+__device__ __forceinline__ void store_row_bf16(__nv_bfloat16* dst, const uint32_t* pk) {
+  uint4* o = reinterpret_cast<uint4*>(dst);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o[j] = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+}
+
+// What the adapters' K steps need; tmT: t (units * 128 rows, 2 rankp), tmU: up (n_adapters, N, rank).
+struct LoraTail {
+  const CUtensorMap* tmT;
+  const CUtensorMap* tmU;
+  Krea2Lora l;
+  int rankp;
+};
+enum { STAGE_LORA = 1, STAGE_LAST = 2 };
+
+template <int BN, int EPI, bool LORA>
+__device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmC,
+                                          const GemmParams& p, const LoraTail& lt) {
   using Cfg = GemmCfg<BN>;
   constexpr int STAGES = Cfg::STAGES;
 
@@ -127,6 +149,9 @@ __global__ void __launch_bounds__(gemm_threads<EPI>(), 1)
   __shared__ __align__(8) uint64_t drain_bar;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
+  // LORA: what each stage holds, written by the producer before the stage's full barrier, read by
+  // the MMA thread after it
+  __shared__ int stage_kind[LORA ? STAGES : 1];
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -155,8 +180,13 @@ __global__ void __launch_bounds__(gemm_threads<EPI>(), 1)
   const uint32_t tmem_base = tmem_slot;
   volatile int* abort = &abort_flag;
 
-  const TileMap tm{p.tiles_m, p.tiles_n, p.group_m};
-  const int total = p.tiles_m * p.tiles_n;
+  int M = p.M, tiles_m = p.tiles_m;
+  if constexpr (LORA) {
+    M = used_rows(lt.l, p.M);
+    tiles_m = (M + BM - 1) / BM;
+  }
+  const TileMap tm{tiles_m, p.tiles_n, p.group_m};
+  const int total = tiles_m * p.tiles_n;
   const int nk = p.K / BK;
 
   if (warp == 0) {
@@ -166,9 +196,14 @@ __global__ void __launch_bounds__(gemm_threads<EPI>(), 1)
       for (int t = blockIdx.x; t < total; t += gridDim.x) {
         int mt, nt;
         tm.map(t, mt, nt);
+        LoraUnit unit;
         for (int kb = 0; kb < nk; ++kb) {
           if (!mbar_wait(&empty_bar[stage], phase ^ 1, abort)) goto producer_done;
           uint8_t* sa = base + stage * Cfg::STAGE_BYTES;
+          if constexpr (LORA) {
+            const bool last = kb == nk - 1 && !(unit = first_unit(lt.l, M, mt)).exists();
+            stage_kind[stage] = last ? STAGE_LAST : 0;
+          }
           mbar_arrive_expect_tx(&full_bar[stage], Cfg::STAGE_BYTES);
           tma_load_2d(sa, &tmA, &full_bar[stage], kb * BK, mt * BM);
           tma_load_2d(sa + Cfg::A_BYTES, &tmB, &full_bar[stage], kb * BK, nt * BN);
@@ -178,10 +213,33 @@ __global__ void __launch_bounds__(gemm_threads<EPI>(), 1)
             phase ^= 1;
           }
         }
+        if constexpr (LORA) {
+          const int chunks = lora_chunks(lt.rankp), up_chunks = (lt.rankp + 63) / 64;
+          if (unit.exists()) lora_wait_prior_grid();  // t is written by the grid before this one
+          while (unit.exists()) {
+            const LoraUnit next = next_unit(lt.l, M, mt, unit);
+            for (int c = 0; c < chunks; ++c) {
+              if (!mbar_wait(&empty_bar[stage], phase ^ 1, abort)) goto producer_done;
+              uint8_t* sa = base + stage * Cfg::STAGE_BYTES;
+              stage_kind[stage] = STAGE_LORA | (c == chunks - 1 && !next.exists() ? STAGE_LAST : 0);
+              mbar_arrive_expect_tx(&full_bar[stage], Cfg::STAGE_BYTES);
+              tma_load_2d(sa, lt.tmT, &full_bar[stage], c * 64, (mt + unit.r) * BM);
+              tma_load_3d(sa + Cfg::A_BYTES, lt.tmU, &full_bar[stage], (c % up_chunks) * 64, nt * BN, unit.adapter);
+              fills.note(stage, phase);
+              if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1;
+              }
+            }
+            unit = next;
+          }
+        }
       }
     producer_done:
       // a wait expired somewhere: let the copies this thread issued land before the CTA exits
       if (*abort) fills.drain(full_bar, STAGES);
+      // no CTA ends before the grid that writes t has, so the next launch in the stream follows both
+      if constexpr (LORA) lora_wait_prior_grid();
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -199,7 +257,8 @@ __global__ void __launch_bounds__(gemm_threads<EPI>(), 1)
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BN;
         bool ok = true;
-        for (int kb = 0; kb < nk; ++kb) {
+        int kind = 0;
+        for (int kb = 0; LORA ? !(kind & STAGE_LAST) : kb < nk; ++kb) {
           if (!mbar_wait(&full_bar[stage], phase, abort)) {
             ok = false;
             break;
@@ -207,8 +266,16 @@ __global__ void __launch_bounds__(gemm_threads<EPI>(), 1)
           tc_fence_after();
           const uint64_t ad = da0 + (uint64_t)(stage * (Cfg::STAGE_BYTES >> 4));
           const uint64_t bd = ad + (uint64_t)(Cfg::A_BYTES >> 4);
+          if constexpr (LORA) kind = *(volatile int*)&stage_kind[stage];
+          if (LORA && (kind & STAGE_LORA)) {
+            // columns of t: [high halves | low halves]; each meets the same columns of up
+            const int steps = min(2 * lt.rankp / 16, 4), wrap = min(lt.rankp / 16, 4);
+            for (int k = 0; k < steps; ++k)
+              tc_mma_bf16(d_tmem, ad + 2 * k, bd + 2 * (k >= wrap ? k - wrap : k), Cfg::IDESC, 1u);
+          } else {
 #pragma unroll
-          for (int k = 0; k < BK / 16; ++k) tc_mma_bf16(d_tmem, ad + 2 * k, bd + 2 * k, Cfg::IDESC, (kb | k) != 0);
+            for (int k = 0; k < BK / 16; ++k) tc_mma_bf16(d_tmem, ad + 2 * k, bd + 2 * k, Cfg::IDESC, (kb | k) != 0);
+          }
           issued = true;
           tc_commit(&empty_bar[stage]);
           if (++stage == STAGES) {
@@ -243,14 +310,15 @@ __global__ void __launch_bounds__(gemm_threads<EPI>(), 1)
       if (!mbar_wait(&tfull_bar[acc], acc_phase, abort)) break;
       tc_fence_after();
       const int row = mt * BM + quarter * 32 + lane;
-      const bool row_ok = row < p.M;
+      const bool row_ok = row < M;
       const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * BN;
 
       const int row0 = mt * BM + quarter * 32;
-      const int nrows = min(32, p.M - row0);
+      const int nrows = min(32, M - row0);
       uint8_t* epi_smem = base + STAGES * Cfg::STAGE_BYTES + (warp - 2) * Cfg::EPI_WARP_BYTES;
       uint32_t* xpk = reinterpret_cast<uint32_t*>(epi_smem);
-      const bool rows_in = row0 < p.M;  // warp-uniform: this 32-row block holds output rows
+      const bool rows_in = row0 < M;  // warp-uniform: this 32-row block holds output rows
+      const bool cut = LORA && row0 + 32 > M;  // warp-uniform: stored row by row
       if constexpr (EPI == EPI_STORE) {
         const int n_store = p.n_store ? p.n_store : p.N;
 #pragma unroll 1
@@ -272,13 +340,17 @@ __global__ void __launch_bounds__(gemm_threads<EPI>(), 1)
           uint32_t pk[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) pk[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
-          store_box_bf16(boxes.next(lane), pk, lane, &tmC, nt * BN + c * 64, row0, rows_in);
+          if (cut) {
+            if (row_ok) store_row_bf16(reinterpret_cast<__nv_bfloat16*>(p.out) + (size_t)row * p.N + nt * BN + c * 64, pk);
+          } else {
+            store_box_bf16(boxes.next(lane), pk, lane, &tmC, nt * BN + c * 64, row0, rows_in);
+          }
         }
       } else if constexpr (EPI == EPI_BIAS_ROWMAP) {
         // fp32 out[map(row), col] = acc + bias[col], rows transposed through shared memory like the
         // residual epilogue below; lane i holds the destination row of tile row row0 + i
         float* xp = reinterpret_cast<float*>(xpk);
-        const int rr = min(row0 + lane, p.M - 1);
+        const int rr = min(row0 + lane, M - 1);
         const long long my_dst = (long long)(rr / p.map_N) * p.map_S + p.map_T + rr % p.map_N;
 #pragma unroll 1
         for (int c = 0; c < BN / 32; ++c) {
@@ -312,7 +384,12 @@ __global__ void __launch_bounds__(gemm_threads<EPI>(), 1)
             for (int e = 0; e < 16; ++e)
               pk[half * 16 + e] = pack_bf16x2(silu_f(gv[2 * e]) * uv[2 * e], silu_f(gv[2 * e + 1]) * uv[2 * e + 1]);
           }
-          store_box_bf16(boxes.next(lane), pk, lane, &tmC, nt * (BN / 2) + g * 64, row0, rows_in);
+          if (cut) {
+            if (row_ok)
+              store_row_bf16(reinterpret_cast<__nv_bfloat16*>(p.out) + (size_t)row * (p.N / 2) + nt * (BN / 2) + g * 64, pk);
+          } else {
+            store_box_bf16(boxes.next(lane), pk, lane, &tmC, nt * (BN / 2) + g * 64, row0, rows_in);
+          }
         }
       } else if constexpr (EPI == EPI_QKV) {
         // [q | k | v | gate] columns; 128-wide q/k heads get RMSNorm (1 + w) and RoPE here,
@@ -381,7 +458,10 @@ __global__ void __launch_bounds__(gemm_threads<EPI>(), 1)
         // Lane i knows the batch row of tile row row0 + i (clamped to M - 1, so that rows of the
         // ragged last tile read an in-bounds gate; their results are never stored).
         float* xp = reinterpret_cast<float*>(base + STAGES * Cfg::STAGE_BYTES) + (warp - 2) * (32 * 32);
-        const int my_b = min(row0 + lane, p.M - 1) / p.rows_per_batch;
+        const int my_row = min(row0 + lane, M - 1);
+        int my_b;
+        if (LORA && p.rows_per_batch == 0) my_b = request_of_row(lt.l.row_start, lt.l.R, my_row);
+        else my_b = my_row / p.rows_per_batch;
 #pragma unroll 1
         for (int c = part * (BN / 64); c < (part + 1) * (BN / 64); ++c) {
           float v[32];
@@ -421,6 +501,21 @@ __global__ void __launch_bounds__(gemm_threads<EPI>(), 1)
     tc_fence_after();
     tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
   }
+}
+
+template <int BN, int EPI>
+__global__ void __launch_bounds__(gemm_threads<EPI>(), 1)
+    gemm_bf16_tcgen05_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                             const __grid_constant__ CUtensorMap tmC, GemmParams p) {
+  gemm_body<BN, EPI, false>(tmA, tmB, tmC, p, LoraTail{});
+}
+
+template <int BN, int EPI>
+__global__ void __launch_bounds__(gemm_threads<EPI>(), 1)
+    gemm_lora_tcgen05_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                             const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmT,
+                             const __grid_constant__ CUtensorMap tmU, GemmParams p, Krea2Lora l, int rankp) {
+  gemm_body<BN, EPI, true>(tmA, tmB, tmC, p, LoraTail{&tmT, &tmU, l, rankp});
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
@@ -539,6 +634,52 @@ int launch_gemm_bn(const GemmParams& p0, const void* A, const void* W, cudaStrea
   return KREA2_OK;
 }
 
+// The GEMM with the adapters' K steps, launched as a programmatic dependent of lora_down: its CTAs
+// start as soon as every lora_down CTA runs, and wait for t only when they first load it.
+template <int BN, int EPI>
+int launch_gemm_lora_bn(const GemmParams& p0, const void* A, const void* W, const Krea2Lora& l, const void* t,
+                        cudaStream_t stream) {
+  using Cfg = GemmCfg<BN>;
+  static std::atomic<uint64_t> attr_done{0};
+  auto kern = gemm_lora_tcgen05_kernel<BN, EPI>;
+  const uint64_t dev_bit = device_bit();
+  if (!(attr_done.load(std::memory_order_acquire) & dev_bit) || !dev_bit) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES) != cudaSuccess)
+      return set_error(KREA2_ERR_CUDA, "cudaFuncSetAttribute(gemm with adapters) failed");
+    attr_done.fetch_or(dev_bit, std::memory_order_release);
+  }
+  GemmParams p = p0;
+  p.tiles_m = (p.M + BM - 1) / BM;
+  p.tiles_n = p.N / BN;
+  p.group_m = group_rows(p.tiles_m, p.K, BN, num_sms());
+  const int rankp = lora_rankp(l.rank);
+  CUtensorMap ta, tb, tc, tt, tu;
+  int rc;
+  if ((rc = make_tmap_bf16_2d(&ta, A, p.K, p.M, p.K, BK, BM))) return rc;
+  if ((rc = make_tmap_bf16_2d(&tb, W, p.K, p.N, p.K, BK, BN))) return rc;
+  if ((rc = make_tmap_bf16_2d(&tt, t, 2 * rankp, (uint64_t)lora_units(p.M, l.R) * BM, 2 * rankp, 64, BM))) return rc;
+  if ((rc = make_tmap_bf16_3d(&tu, l.up, l.rank, p.N, l.n_adapters, l.rank, 64, BN, p.N))) return rc;
+  memset(&tc, 0, sizeof(tc));
+  const int out_cols = EPI == EPI_SWIGLU ? p.N / 2 : p.N;
+  if constexpr (EPI != EPI_RESID)
+    if ((rc = make_tmap_bf16_2d(&tc, p.out, out_cols, p.M, out_cols, 64, 32))) return rc;
+  const int total = p.tiles_m * p.tiles_n;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(total < num_sms() ? total : num_sms());
+  cfg.blockDim = dim3(gemm_threads<EPI>());
+  cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, ta, tb, tc, tt, tu, p, l, rankp);
+  count_launch();
+  if (e != cudaSuccess) return set_error(KREA2_ERR_CUDA, "gemm with adapters launch failed: %s", cudaGetErrorString(e));
+  return KREA2_OK;
+}
+
 // Wave efficiency of a tile count on the SMs (1.0 = every wave full).
 double wave_eff(long tiles, int sms) {
   long waves = (tiles + sms - 1) / sms;
@@ -575,6 +716,30 @@ int gemm_bf16(int epi, const GemmParams& p, const void* A, const void* W, cudaSt
     case EPI_BIAS_ROWMAP: return launch_gemm_bn<128, EPI_BIAS_ROWMAP>(p, A, W, stream);
     default: return launch_gemm_bn<128, EPI_RESID>(p, A, W, stream);
   }
+}
+
+int gemm_bf16_lora(int epi, const GemmParams& p, const void* A, const void* W, const Krea2Lora& l, const void* t,
+                   cudaStream_t stream) {
+  const int sms = num_sms();
+  const long tm = (p.M + BM - 1) / BM;
+  const double e128 = wave_eff(tm * (p.N / 128), sms);
+  int bn = 128;
+  if (p.N % 256 == 0 && (wave_eff(tm * (p.N / 256), sms) >= 0.8 * e128 || tm * (p.N / 256) >= 4L * sms)) bn = 256;
+  // few tiles: narrower ones put more SMs on the stream of W (a SwiGLU tile is 128 columns at least)
+  if (bn == 128 && epi != EPI_SWIGLU && wave_eff(tm * (p.N / 64), sms) > 1.25 * e128) bn = 64;
+#define KREA2_GEMM_LORA(E)                                                              \
+  return bn == 256 ? launch_gemm_lora_bn<256, E>(p, A, W, l, t, stream)                 \
+                   : launch_gemm_lora_bn<128, E>(p, A, W, l, t, stream)
+  switch (epi) {
+    case EPI_STORE:
+      if (bn == 64) return launch_gemm_lora_bn<64, EPI_STORE>(p, A, W, l, t, stream);
+      KREA2_GEMM_LORA(EPI_STORE);
+    case EPI_SWIGLU: KREA2_GEMM_LORA(EPI_SWIGLU);
+    default:
+      if (bn == 64) return launch_gemm_lora_bn<64, EPI_RESID>(p, A, W, l, t, stream);
+      KREA2_GEMM_LORA(EPI_RESID);
+  }
+#undef KREA2_GEMM_LORA
 }
 
 }  // namespace krea2

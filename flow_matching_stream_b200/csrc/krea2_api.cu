@@ -295,10 +295,10 @@ const char* krea2_last_error_string(void) { return g_err; }
 int krea2_check_device_error(void* stream) {
   cudaError_t e = cudaStreamSynchronize(as_stream(stream));
   if (e != cudaSuccess) return set_error(KREA2_ERR_CUDA, "stream error: %s", cudaGetErrorString(e));
-  constexpr int FILES = 4;
+  constexpr int FILES = 5;
   const int ve[FILES] = {take_device_error_gemm(), take_device_error_attention(), take_device_error_paged(),
-                         take_device_error_lora()};
-  const char* names[FILES] = {"GEMM", "attention", "paged cache", "adapter"};
+                         take_device_error_lora(), take_device_error_lora_tc()};
+  const char* names[FILES] = {"GEMM", "attention", "paged cache", "adapter", "adapter"};
   for (int i = 0; i < FILES; ++i) {
     if (ve[i] < 0) return set_error(KREA2_ERR_CUDA, "cannot read the device error word");
     if (ve[i] & ERR_WAIT_TIMEOUT)

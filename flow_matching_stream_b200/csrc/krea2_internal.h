@@ -31,6 +31,7 @@ int take_device_error_gemm();
 int take_device_error_attention();
 int take_device_error_paged();
 int take_device_error_lora();
+int take_device_error_lora_tc();
 
 struct GemmParams {
   int M, N, K;              // N = rows of W
@@ -181,6 +182,11 @@ struct LoraLinearArgs {
   int rows_per_batch;     // RESID: 0 takes the gate row of the row's request
   long long gate_stride;
 };
+// tensor-core path: t (lora_t_bytes) by launch_lora_down_tc, then the GEMM with the adapters' K steps
+size_t lora_t_bytes(int M, int R, int rank);
+int launch_lora_down_tc(const void* A, int M, int K, const Krea2Lora& l, void* t, cudaStream_t stream);
+int gemm_bf16_lora(int epi, const GemmParams& p, const void* A, const void* W, const Krea2Lora& l, const void* t,
+                   cudaStream_t stream);
 size_t lora_workspace_bytes(int dtype, int epi, int M, int N, int K, int R, int rank);
 int launch_lora_linear(int dtype, int epi, const LoraLinearArgs& a, const Krea2Lora& l, void* ws, cudaStream_t stream);
 
