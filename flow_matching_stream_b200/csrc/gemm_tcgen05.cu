@@ -132,26 +132,31 @@ struct LoraTail {
   const CUtensorMap* tmU;
   Krea2Lora l;
   int rankp;
+  // A stage holds kch K steps (64 columns each): A's chunks a_pitch bytes apart, then W's.
+  int kch, a_pitch, stage_bytes, stages;
 };
-enum { STAGE_LORA = 1, STAGE_LAST = 2 };
+constexpr int MAX_STAGES = 8;
 
 template <int BN, int EPI, bool LORA>
 __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmC,
                                           const GemmParams& p, const LoraTail& lt) {
   using Cfg = GemmCfg<BN>;
-  constexpr int STAGES = Cfg::STAGES;
+  const int STAGES = LORA ? lt.stages : Cfg::STAGES;
+  const int stage_bytes = LORA ? lt.stage_bytes : Cfg::STAGE_BYTES;
+  const int kch = LORA ? lt.kch : 1;
+  const int w_off = LORA ? lt.kch * lt.a_pitch : Cfg::A_BYTES;  // W's part of a stage
 
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full_bar[STAGES];
-  __shared__ __align__(8) uint64_t empty_bar[STAGES];
+  __shared__ __align__(8) uint64_t full_bar[LORA ? MAX_STAGES : Cfg::STAGES];
+  __shared__ __align__(8) uint64_t empty_bar[LORA ? MAX_STAGES : Cfg::STAGES];
   __shared__ __align__(8) uint64_t tfull_bar[2];
   __shared__ __align__(8) uint64_t tempty_bar[2];
   __shared__ __align__(8) uint64_t drain_bar;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
-  // LORA: what each stage holds, written by the producer before the stage's full barrier, read by
-  // the MMA thread after it
-  __shared__ int stage_kind[LORA ? STAGES : 1];
+  // LORA: whether the tile has a K step after this stage's (from the last step of K on), written by the
+  // producer before the stage's full barrier, read by the MMA thread after it
+  __shared__ int stage_more[LORA ? MAX_STAGES : 1];
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -187,7 +192,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
   }
   const TileMap tm{tiles_m, p.tiles_n, p.group_m};
   const int total = tiles_m * p.tiles_n;
-  const int nk = p.K / BK;
+  const int nk = (p.K / BK + kch - 1) / kch;  // stages of a tile (chunks past K read as zeros)
 
   if (warp == 0) {
     if (lane == 0) {
@@ -199,14 +204,19 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
         LoraUnit unit;
         for (int kb = 0; kb < nk; ++kb) {
           if (!mbar_wait(&empty_bar[stage], phase ^ 1, abort)) goto producer_done;
-          uint8_t* sa = base + stage * Cfg::STAGE_BYTES;
-          if constexpr (LORA) {
-            const bool last = kb == nk - 1 && !(unit = first_unit(lt.l, M, mt)).exists();
-            stage_kind[stage] = last ? STAGE_LAST : 0;
+          uint8_t* sa = base + stage * stage_bytes;
+          if (LORA && kb == nk - 1) {
+            unit = first_unit(lt.l, M, mt);
+            stage_more[stage] = unit.exists();
           }
-          mbar_arrive_expect_tx(&full_bar[stage], Cfg::STAGE_BYTES);
-          tma_load_2d(sa, &tmA, &full_bar[stage], kb * BK, mt * BM);
-          tma_load_2d(sa + Cfg::A_BYTES, &tmB, &full_bar[stage], kb * BK, nt * BN);
+          mbar_arrive_expect_tx(&full_bar[stage], stage_bytes);
+          if constexpr (LORA) {
+            tma_load_4d(sa, &tmA, &full_bar[stage], 0, mt * BM, kb * kch, 0);
+            tma_load_4d(sa + w_off, &tmB, &full_bar[stage], 0, nt * BN, kb * kch, 0);
+          } else {
+            tma_load_2d(sa, &tmA, &full_bar[stage], kb * BK, mt * BM);
+            tma_load_2d(sa + Cfg::A_BYTES, &tmB, &full_bar[stage], kb * BK, nt * BN);
+          }
           fills.note(stage, phase);
           if (++stage == STAGES) {
             stage = 0;
@@ -220,11 +230,11 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
             const LoraUnit next = next_unit(lt.l, M, mt, unit);
             for (int c = 0; c < chunks; ++c) {
               if (!mbar_wait(&empty_bar[stage], phase ^ 1, abort)) goto producer_done;
-              uint8_t* sa = base + stage * Cfg::STAGE_BYTES;
-              stage_kind[stage] = STAGE_LORA | (c == chunks - 1 && !next.exists() ? STAGE_LAST : 0);
-              mbar_arrive_expect_tx(&full_bar[stage], Cfg::STAGE_BYTES);
+              uint8_t* sa = base + stage * stage_bytes;
+              stage_more[stage] = c < chunks - 1 || next.exists();
+              mbar_arrive_expect_tx(&full_bar[stage], lt.a_pitch + Cfg::B_BYTES);
               tma_load_2d(sa, lt.tmT, &full_bar[stage], c * 64, (mt + unit.r) * BM);
-              tma_load_3d(sa + Cfg::A_BYTES, lt.tmU, &full_bar[stage], (c % up_chunks) * 64, nt * BN, unit.adapter);
+              tma_load_3d(sa + w_off, lt.tmU, &full_bar[stage], (c % up_chunks) * 64, nt * BN, unit.adapter);
               fills.note(stage, phase);
               if (++stage == STAGES) {
                 stage = 0;
@@ -257,30 +267,51 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BN;
         bool ok = true;
-        int kind = 0;
-        for (int kb = 0; LORA ? !(kind & STAGE_LAST) : kb < nk; ++kb) {
+        int more = 0;
+        for (int kb = 0; kb < nk; ++kb) {
           if (!mbar_wait(&full_bar[stage], phase, abort)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t ad = da0 + (uint64_t)(stage * (Cfg::STAGE_BYTES >> 4));
-          const uint64_t bd = ad + (uint64_t)(Cfg::A_BYTES >> 4);
-          if constexpr (LORA) kind = *(volatile int*)&stage_kind[stage];
-          if (LORA && (kind & STAGE_LORA)) {
-            // columns of t: [high halves | low halves]; each meets the same columns of up
-            const int steps = min(2 * lt.rankp / 16, 4), wrap = min(lt.rankp / 16, 4);
-            for (int k = 0; k < steps; ++k)
-              tc_mma_bf16(d_tmem, ad + 2 * k, bd + 2 * (k >= wrap ? k - wrap : k), Cfg::IDESC, 1u);
-          } else {
+          uint64_t ad = da0 + (uint64_t)(stage * (stage_bytes >> 4));
+          uint64_t bd = ad + (uint64_t)(w_off >> 4);
 #pragma unroll
-            for (int k = 0; k < BK / 16; ++k) tc_mma_bf16(d_tmem, ad + 2 * k, bd + 2 * k, Cfg::IDESC, (kb | k) != 0);
-          }
+          for (int k = 0; k < BK / 16; ++k) tc_mma_bf16(d_tmem, ad + 2 * k, bd + 2 * k, Cfg::IDESC, (kb | k) != 0);
+          if constexpr (LORA)
+            for (int c = 1; c < kch; ++c) {
+              ad += lt.a_pitch >> 4;
+              bd += Cfg::B_BYTES >> 4;
+#pragma unroll
+              for (int k = 0; k < BK / 16; ++k) tc_mma_bf16(d_tmem, ad + 2 * k, bd + 2 * k, Cfg::IDESC, 1u);
+            }
           issued = true;
+          if (LORA && kb == nk - 1) more = *(volatile int*)&stage_more[stage];
           tc_commit(&empty_bar[stage]);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
+          }
+        }
+        if constexpr (LORA) {
+          // columns of t: [high halves | low halves]; each meets the same columns of up
+          const int steps = min(2 * lt.rankp / 16, 4), wrap = min(lt.rankp / 16, 4);
+          while (ok && more) {
+            if (!mbar_wait(&full_bar[stage], phase, abort)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t ad = da0 + (uint64_t)(stage * (stage_bytes >> 4));
+            const uint64_t bd = ad + (uint64_t)(w_off >> 4);
+            for (int k = 0; k < steps; ++k)
+              tc_mma_bf16(d_tmem, ad + 2 * k, bd + 2 * (k >= wrap ? k - wrap : k), Cfg::IDESC, 1u);
+            more = *(volatile int*)&stage_more[stage];
+            tc_commit(&empty_bar[stage]);
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1;
+            }
           }
         }
         if (!ok) break;
@@ -300,7 +331,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
     // second four warps, which take the other half of the columns)
     const int quarter = warp & 3;
     const int part = (warp - 2) >> 2;
-    EpiBoxes boxes{base + STAGES * Cfg::STAGE_BYTES + (warp - 2) * Cfg::EPI_WARP_BYTES, 0};
+    EpiBoxes boxes{base + Cfg::STAGES * Cfg::STAGE_BYTES + (warp - 2) * Cfg::EPI_WARP_BYTES, 0};
     int local = 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x, ++local) {
       int mt, nt;
@@ -315,7 +346,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
 
       const int row0 = mt * BM + quarter * 32;
       const int nrows = min(32, M - row0);
-      uint8_t* epi_smem = base + STAGES * Cfg::STAGE_BYTES + (warp - 2) * Cfg::EPI_WARP_BYTES;
+      uint8_t* epi_smem = base + Cfg::STAGES * Cfg::STAGE_BYTES + (warp - 2) * Cfg::EPI_WARP_BYTES;
       uint32_t* xpk = reinterpret_cast<uint32_t*>(epi_smem);
       const bool rows_in = row0 < M;  // warp-uniform: this 32-row block holds output rows
       const bool cut = LORA && row0 + 32 > M;  // warp-uniform: stored row by row
@@ -457,7 +488,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
         // part 0 takes the tile's first BN / 2 columns, part 1 the rest.
         // Lane i knows the batch row of tile row row0 + i (clamped to M - 1, so that rows of the
         // ragged last tile read an in-bounds gate; their results are never stored).
-        float* xp = reinterpret_cast<float*>(base + STAGES * Cfg::STAGE_BYTES) + (warp - 2) * (32 * 32);
+        float* xp = reinterpret_cast<float*>(base + Cfg::STAGES * Cfg::STAGE_BYTES) + (warp - 2) * (32 * 32);
         const int my_row = min(row0 + lane, M - 1);
         int my_b;
         if (LORA && p.rows_per_batch == 0) my_b = request_of_row(lt.l.row_start, lt.l.R, my_row);
@@ -514,8 +545,10 @@ template <int BN, int EPI>
 __global__ void __launch_bounds__(gemm_threads<EPI>(), 1)
     gemm_lora_tcgen05_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                              const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmT,
-                             const __grid_constant__ CUtensorMap tmU, GemmParams p, Krea2Lora l, int rankp) {
-  gemm_body<BN, EPI, true>(tmA, tmB, tmC, p, LoraTail{&tmT, &tmU, l, rankp});
+                             const __grid_constant__ CUtensorMap tmU, GemmParams p, LoraTail lt) {
+  lt.tmT = &tmT;
+  lt.tmU = &tmU;
+  gemm_body<BN, EPI, true>(tmA, tmB, tmC, p, lt);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
@@ -548,6 +581,25 @@ int make_tmap_bf16_2d(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t r
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return set_error(KREA2_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return KREA2_OK;
+}
+
+// Row-major bf16 matrices (batches, rows, cols), cols a multiple of 64, viewed as (batches, chunks of 64 columns,
+// rows, 64): a box is box_chunks K-major operand tiles of box_rows x 64, one behind the other in shared memory.
+// Chunks and rows past the matrix read as zeros.
+int make_tmap_bf16_chunks(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t batches,
+                          uint32_t box_rows, uint32_t box_chunks) {
+  auto enc = get_encode_fn();
+  if (!enc) return set_error(KREA2_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  if (reinterpret_cast<uintptr_t>(ptr) & 15) return set_error(KREA2_ERR_ARG, "TMA operand must be 16-byte aligned");
+  cuuint64_t dims[4] = {64, rows, cols / 64, batches};
+  cuuint64_t strides[3] = {cols * 2, 128, rows * cols * 2};
+  cuuint32_t box[4] = {64, box_rows, box_chunks, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(KREA2_ERR_CUDA, "cuTensorMapEncodeTiled (chunks) failed (%d)", (int)r);
   return KREA2_OK;
 }
 
@@ -652,12 +704,29 @@ int launch_gemm_lora_bn(const GemmParams& p0, const void* A, const void* W, cons
   p.tiles_m = (p.M + BM - 1) / BM;
   p.tiles_n = p.N / BN;
   p.group_m = group_rows(p.tiles_m, p.K, BN, num_sms());
-  const int rankp = lora_rankp(l.rank);
+  LoraTail lt{};
+  lt.l = l;
+  lt.rankp = lora_rankp(l.rank);
+  // Rows past M would be zero-filled; the accumulator rows that other shared memory gives instead are
+  // not stored (the MMA reads 128 rows from each chunk on, which ends inside the ring or the epilogue's boxes).
+  const int a_rows = p.M < BM ? (p.M + 7) / 8 * 8 : BM;
+  lt.a_pitch = a_rows * BK * 2;
+  // One row tile streams W once, and a stage's turn (a wait, a load of A and one of W by one thread) takes
+  // about 0.3 us whatever it loads: stages of several K steps, as many as leave three stages. 6144 x 6144 by
+  // one row: 34 us with one K step a stage.
+  lt.kch = 1;
+  if (p.tiles_m == 1)
+    for (int c = 4; c > 1 && lt.kch == 1; c /= 2)
+      if (3 * c * (lt.a_pitch + Cfg::B_BYTES) <= Cfg::STAGES * Cfg::STAGE_BYTES) lt.kch = c;
+  lt.stage_bytes = lt.kch * (lt.a_pitch + Cfg::B_BYTES);
+  lt.stages = Cfg::STAGES * Cfg::STAGE_BYTES / lt.stage_bytes;
+  if (lt.stages > MAX_STAGES) lt.stages = MAX_STAGES;
   CUtensorMap ta, tb, tc, tt, tu;
   int rc;
-  if ((rc = make_tmap_bf16_2d(&ta, A, p.K, p.M, p.K, BK, BM))) return rc;
-  if ((rc = make_tmap_bf16_2d(&tb, W, p.K, p.N, p.K, BK, BN))) return rc;
-  if ((rc = make_tmap_bf16_2d(&tt, t, 2 * rankp, (uint64_t)lora_units(p.M, l.R) * BM, 2 * rankp, 64, BM))) return rc;
+  if ((rc = make_tmap_bf16_chunks(&ta, A, p.K, p.M, 1, a_rows, lt.kch))) return rc;
+  if ((rc = make_tmap_bf16_chunks(&tb, W, p.K, p.N, 1, BN, lt.kch))) return rc;
+  if ((rc = make_tmap_bf16_2d(&tt, t, 2 * lt.rankp, (uint64_t)lora_units(p.M, l.R) * BM, 2 * lt.rankp, 64, a_rows)))
+    return rc;
   if ((rc = make_tmap_bf16_3d(&tu, l.up, l.rank, p.N, l.n_adapters, l.rank, 64, BN, p.N))) return rc;
   memset(&tc, 0, sizeof(tc));
   const int out_cols = EPI == EPI_SWIGLU ? p.N / 2 : p.N;
@@ -674,7 +743,7 @@ int launch_gemm_lora_bn(const GemmParams& p0, const void* A, const void* W, cons
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, ta, tb, tc, tt, tu, p, l, rankp);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, ta, tb, tc, tt, tu, p, lt);
   count_launch();
   if (e != cudaSuccess) return set_error(KREA2_ERR_CUDA, "gemm with adapters launch failed: %s", cudaGetErrorString(e));
   return KREA2_OK;

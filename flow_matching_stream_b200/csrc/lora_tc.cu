@@ -14,17 +14,17 @@
 
 namespace krea2 {
 
-int make_tmap_bf16_2d(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t row_stride_elems,
-                      uint32_t box_cols, uint32_t box_rows);
-int make_tmap_bf16_3d(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t batches,
-                      uint64_t row_stride_elems, uint32_t box_cols, uint32_t box_rows, uint64_t batch_rows);
+int make_tmap_bf16_chunks(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t batches,
+                          uint32_t box_rows, uint32_t box_chunks);
 
 KREA2_DEFINE_ERROR_READER(take_device_error_lora_tc)
 
 namespace {
 
+constexpr int MAX_STAGES = 6;
+// Alignment, and the rows behind a short batch's that an MMA of 128 rows reads past the last stage's.
+constexpr int SMEM_SLACK = 1024 + (8 << 10);
 constexpr int DOWN_THREADS = 192;  // producer, MMA, 4 warps that empty TMEM; all of them reduce
-constexpr int DA_BYTES = 128 * 128;  // A: 128 rows x 64 bf16
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -59,15 +59,16 @@ __device__ __forceinline__ LoraUnit unit_of(const Krea2Lora& l, int M, int u, in
   return x;
 }
 
-// splits: CTAs per cluster; N: rank rounded up to 16.
+// splits: CTAs per cluster; N: rank rounded up to 16; kch: K steps of 64 columns per stage (one thread's
+// turn of a wait and two loads takes about 0.3 us whatever it loads), A's a_pitch bytes apart.
 __global__ void __launch_bounds__(DOWN_THREADS) lora_down_tc_kernel(const __grid_constant__ CUtensorMap tmA,
                                                                     const __grid_constant__ CUtensorMap tmD,
                                                                     Krea2Lora l, int M, int K, int N, int stages,
-                                                                    int splits, int tmem_cols, int rankp,
+                                                                    int splits, int tmem_cols, int rankp, int a_pitch, int kch,
                                                                     __nv_bfloat16* __restrict__ t) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full_bar[8];
-  __shared__ __align__(8) uint64_t empty_bar[8];
+  __shared__ __align__(8) uint64_t full_bar[MAX_STAGES];
+  __shared__ __align__(8) uint64_t empty_bar[MAX_STAGES];
   __shared__ __align__(8) uint64_t done_bar;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
@@ -106,9 +107,9 @@ __global__ void __launch_bounds__(DOWN_THREADS) lora_down_tc_kernel(const __grid
   volatile int* abort = &abort_flag;
   // the GEMM behind this grid may start (it waits for t itself): this CTA has its TMEM
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int nk = K / 64;
+  const int nk = (K / 64 + kch - 1) / kch;  // stages over the whole of K (chunks past it read as zeros)
   const int k0 = (int)((long)split * nk / splits), k1 = (int)((long)(split + 1) * nk / splits);
-  const int stage_bytes = DA_BYTES + N * 128;
+  const int d_off = kch * a_pitch, stage_bytes = d_off + kch * N * 128;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -118,8 +119,8 @@ __global__ void __launch_bounds__(DOWN_THREADS) lora_down_tc_kernel(const __grid
         if (!mbar_wait(&empty_bar[stage], phase ^ 1, abort)) break;
         uint8_t* sa = base + stage * stage_bytes;
         mbar_arrive_expect_tx(&full_bar[stage], stage_bytes);
-        tma_load_2d(sa, &tmA, &full_bar[stage], kb * 64, mt * 128);
-        tma_load_3d(sa + DA_BYTES, &tmD, &full_bar[stage], kb * 64, 0, x.adapter);
+        tma_load_4d(sa, &tmA, &full_bar[stage], 0, mt * 128, kb * kch, 0);
+        tma_load_4d(sa + d_off, &tmD, &full_bar[stage], 0, 0, kb * kch, x.adapter);
         fills.note(stage, phase);
         if (++stage == (uint32_t)stages) {
           stage = 0;
@@ -136,10 +137,11 @@ __global__ void __launch_bounds__(DOWN_THREADS) lora_down_tc_kernel(const __grid
       for (int kb = k0; kb < k1; ++kb) {
         if (!mbar_wait(&full_bar[stage], phase, abort)) break;
         tc_fence_after();
-        const uint64_t ad = da0 + (uint64_t)(stage * (stage_bytes >> 4));
-        const uint64_t bd = ad + (uint64_t)(DA_BYTES >> 4);
+        uint64_t ad = da0 + (uint64_t)(stage * (stage_bytes >> 4));
+        uint64_t bd = ad + (uint64_t)(d_off >> 4);
+        for (int c = 0; c < kch; ++c, ad += a_pitch >> 4, bd += N * 128 >> 4)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) tc_mma_bf16(tmem, ad + 2 * k, bd + 2 * k, idesc, kb > k0 || k > 0);
+          for (int k = 0; k < 4; ++k) tc_mma_bf16(tmem, ad + 2 * k, bd + 2 * k, idesc, kb > k0 || c > 0 || k > 0);
         tc_commit(&empty_bar[stage]);
         if (++stage == (uint32_t)stages) {
           stage = 0;
@@ -208,17 +210,24 @@ size_t lora_t_bytes(int M, int R, int rank) { return (size_t)lora_units(M, R) * 
 int launch_lora_down_tc(const void* A, int M, int K, const Krea2Lora& l, void* t, cudaStream_t stream) {
   const int N = (l.rank + 15) / 16 * 16, rankp = lora_rankp(l.rank);
   const int units = lora_units(M, l.R) - 1;  // the largest unit number is (row tiles - 1) + (R - 1)
-  const int nk = K / 64;
-  int splits = 8;  // enough CTAs to keep the loads of A in flight on every SM
-  while (splits > 1 && (splits > nk || (long)units * (splits / 2) >= 2L * num_sms())) splits /= 2;
-  const int stage_bytes = DA_BYTES + N * 128;
-  int stages = N > 128 ? 4 : 6;
+  const int a_rows = M < 128 ? (M + 7) / 8 * 8 : 128;  // the rows behind them are not used
+  const int a_pitch = a_rows * 128, step = a_pitch + N * 128;
+  const int kch = 4 * step <= (36 << 10) ? 4 : 2 * step <= (48 << 10) ? 2 : 1;
+  const int stage_bytes = kch * step;
+  const int nk = (K / 64 + kch - 1) / kch;
+  // two CTAs fit an SM up to N = 128: as many parts of K as fill the SMs once
+  const int slots = N > 128 ? num_sms() : 2 * num_sms();
+  int splits = slots / units;
+  splits = splits < 1 ? 1 : splits > 8 ? 8 : splits;
+  if (splits > nk) splits = nk;
+  int stages = N > 128 ? 4 : (96 << 10) / stage_bytes;
+  if (stages > MAX_STAGES) stages = MAX_STAGES;
   if (stages > (nk + splits - 1) / splits) stages = (nk + splits - 1) / splits;
   int smem = stages * stage_bytes;
   const int part = 128 * (N + 1) * 4;
   if (smem < part) smem = part;
-  smem += 1024;
-  constexpr int MOST = 4 * (DA_BYTES + 256 * 128) + 1024;  // 197 KB: N = 256; also above 6 stages at N = 128
+  smem += SMEM_SLACK;
+  constexpr int MOST = 4 * (128 + 256) * 128 + SMEM_SLACK;  // N = 256
   static std::atomic<uint64_t> attr_done{0};
   const uint64_t dev_bit = device_bit();
   if (!(attr_done.load(std::memory_order_acquire) & dev_bit) || !dev_bit) {
@@ -228,8 +237,9 @@ int launch_lora_down_tc(const void* A, int M, int K, const Krea2Lora& l, void* t
   }
   CUtensorMap ta, td;
   int rc;
-  if ((rc = make_tmap_bf16_2d(&ta, A, K, M, K, 64, 128))) return rc;
-  if ((rc = make_tmap_bf16_3d(&td, l.down, K, l.rank, l.n_adapters, K, 64, N, l.rank))) return rc;
+  if ((rc = make_tmap_bf16_chunks(&ta, A, K, M, 1, a_rows, kch)) ||
+      (rc = make_tmap_bf16_chunks(&td, l.down, K, l.rank, l.n_adapters, N, kch)))
+    return rc;
   int tmem_cols = 32;
   while (tmem_cols < N) tmem_cols *= 2;
   cudaLaunchConfig_t cfg{};
@@ -243,7 +253,7 @@ int launch_lora_down_tc(const void* A, int M, int K, const Krea2Lora& l, void* t
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, lora_down_tc_kernel, ta, td, l, M, K, N, stages, splits, tmem_cols, rankp,
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, lora_down_tc_kernel, ta, td, l, M, K, N, stages, splits, tmem_cols, rankp, a_pitch, kch,
                                            reinterpret_cast<__nv_bfloat16*>(t));
   count_launch();
   if (e != cudaSuccess) return set_error(KREA2_ERR_CUDA, "lora_down launch failed: %s", cudaGetErrorString(e));
