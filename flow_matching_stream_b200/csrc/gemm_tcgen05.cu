@@ -137,18 +137,19 @@ struct LoraTail {
 };
 constexpr int MAX_STAGES = 8;
 
-template <int BN, int EPI, bool LORA>
+// LORA: the adapters' K steps follow those of K. WIDE (with LORA, one row tile): stages of several K steps.
+template <int BN, int EPI, bool LORA, bool WIDE>
 __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmC,
                                           const GemmParams& p, const LoraTail& lt) {
   using Cfg = GemmCfg<BN>;
-  const int STAGES = LORA ? lt.stages : Cfg::STAGES;
-  const int stage_bytes = LORA ? lt.stage_bytes : Cfg::STAGE_BYTES;
-  const int kch = LORA ? lt.kch : 1;
-  const int w_off = LORA ? lt.kch * lt.a_pitch : Cfg::A_BYTES;  // W's part of a stage
+  const int STAGES = WIDE ? lt.stages : Cfg::STAGES;
+  const int stage_bytes = WIDE ? lt.stage_bytes : Cfg::STAGE_BYTES;
+  const int kch = WIDE ? lt.kch : 1;
+  const int w_off = WIDE ? lt.kch * lt.a_pitch : Cfg::A_BYTES;  // W's part of a stage
 
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full_bar[LORA ? MAX_STAGES : Cfg::STAGES];
-  __shared__ __align__(8) uint64_t empty_bar[LORA ? MAX_STAGES : Cfg::STAGES];
+  __shared__ __align__(8) uint64_t full_bar[WIDE ? MAX_STAGES : Cfg::STAGES];
+  __shared__ __align__(8) uint64_t empty_bar[WIDE ? MAX_STAGES : Cfg::STAGES];
   __shared__ __align__(8) uint64_t tfull_bar[2];
   __shared__ __align__(8) uint64_t tempty_bar[2];
   __shared__ __align__(8) uint64_t drain_bar;
@@ -156,7 +157,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
   __shared__ int abort_flag;
   // LORA: whether the tile has a K step after this stage's (from the last step of K on), written by the
   // producer before the stage's full barrier, read by the MMA thread after it
-  __shared__ int stage_more[LORA ? MAX_STAGES : 1];
+  __shared__ int stage_more[WIDE ? MAX_STAGES : LORA ? Cfg::STAGES : 1];
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -210,7 +211,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
             stage_more[stage] = unit.exists();
           }
           mbar_arrive_expect_tx(&full_bar[stage], stage_bytes);
-          if constexpr (LORA) {
+          if constexpr (WIDE) {
             tma_load_4d(sa, &tmA, &full_bar[stage], 0, mt * BM, kb * kch, 0);
             tma_load_4d(sa + w_off, &tmB, &full_bar[stage], 0, nt * BN, kb * kch, 0);
           } else {
@@ -232,7 +233,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
               if (!mbar_wait(&empty_bar[stage], phase ^ 1, abort)) goto producer_done;
               uint8_t* sa = base + stage * stage_bytes;
               stage_more[stage] = c < chunks - 1 || next.exists();
-              mbar_arrive_expect_tx(&full_bar[stage], lt.a_pitch + Cfg::B_BYTES);
+              mbar_arrive_expect_tx(&full_bar[stage], (WIDE ? lt.a_pitch : Cfg::A_BYTES) + Cfg::B_BYTES);
               tma_load_2d(sa, lt.tmT, &full_bar[stage], c * 64, (mt + unit.r) * BM);
               tma_load_3d(sa + w_off, lt.tmU, &full_bar[stage], (c % up_chunks) * 64, nt * BN, unit.adapter);
               fills.note(stage, phase);
@@ -278,7 +279,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
           uint64_t bd = ad + (uint64_t)(w_off >> 4);
 #pragma unroll
           for (int k = 0; k < BK / 16; ++k) tc_mma_bf16(d_tmem, ad + 2 * k, bd + 2 * k, Cfg::IDESC, (kb | k) != 0);
-          if constexpr (LORA)
+          if constexpr (WIDE)
             for (int c = 1; c < kch; ++c) {
               ad += lt.a_pitch >> 4;
               bd += Cfg::B_BYTES >> 4;
@@ -538,17 +539,17 @@ template <int BN, int EPI>
 __global__ void __launch_bounds__(gemm_threads<EPI>(), 1)
     gemm_bf16_tcgen05_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                              const __grid_constant__ CUtensorMap tmC, GemmParams p) {
-  gemm_body<BN, EPI, false>(tmA, tmB, tmC, p, LoraTail{});
+  gemm_body<BN, EPI, false, false>(tmA, tmB, tmC, p, LoraTail{});
 }
 
-template <int BN, int EPI>
+template <int BN, int EPI, bool WIDE>
 __global__ void __launch_bounds__(gemm_threads<EPI>(), 1)
     gemm_lora_tcgen05_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                              const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmT,
                              const __grid_constant__ CUtensorMap tmU, GemmParams p, LoraTail lt) {
   lt.tmT = &tmT;
   lt.tmU = &tmU;
-  gemm_body<BN, EPI, true>(tmA, tmB, tmC, p, lt);
+  gemm_body<BN, EPI, true, WIDE>(tmA, tmB, tmC, p, lt);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
@@ -688,12 +689,12 @@ int launch_gemm_bn(const GemmParams& p0, const void* A, const void* W, cudaStrea
 
 // The GEMM with the adapters' K steps, launched as a programmatic dependent of lora_down: its CTAs
 // start as soon as every lora_down CTA runs, and wait for t only when they first load it.
-template <int BN, int EPI>
+template <int BN, int EPI, bool WIDE>
 int launch_gemm_lora_bn(const GemmParams& p0, const void* A, const void* W, const Krea2Lora& l, const void* t,
                         cudaStream_t stream) {
   using Cfg = GemmCfg<BN>;
   static std::atomic<uint64_t> attr_done{0};
-  auto kern = gemm_lora_tcgen05_kernel<BN, EPI>;
+  auto kern = gemm_lora_tcgen05_kernel<BN, EPI, WIDE>;
   const uint64_t dev_bit = device_bit();
   if (!(attr_done.load(std::memory_order_acquire) & dev_bit) || !dev_bit) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES) != cudaSuccess)
@@ -707,24 +708,27 @@ int launch_gemm_lora_bn(const GemmParams& p0, const void* A, const void* W, cons
   LoraTail lt{};
   lt.l = l;
   lt.rankp = lora_rankp(l.rank);
-  // Rows past M would be zero-filled; the accumulator rows that other shared memory gives instead are
-  // not stored (the MMA reads 128 rows from each chunk on, which ends inside the ring or the epilogue's boxes).
-  const int a_rows = p.M < BM ? (p.M + 7) / 8 * 8 : BM;
-  lt.a_pitch = a_rows * BK * 2;
-  // One row tile streams W once, and a stage's turn (a wait, a load of A and one of W by one thread) takes
-  // about 0.3 us whatever it loads: stages of several K steps, as many as leave three stages. 6144 x 6144 by
-  // one row: 34 us with one K step a stage.
-  lt.kch = 1;
-  if (p.tiles_m == 1)
-    for (int c = 4; c > 1 && lt.kch == 1; c /= 2)
-      if (3 * c * (lt.a_pitch + Cfg::B_BYTES) <= Cfg::STAGES * Cfg::STAGE_BYTES) lt.kch = c;
-  lt.stage_bytes = lt.kch * (lt.a_pitch + Cfg::B_BYTES);
-  lt.stages = Cfg::STAGES * Cfg::STAGE_BYTES / lt.stage_bytes;
-  if (lt.stages > MAX_STAGES) lt.stages = MAX_STAGES;
   CUtensorMap ta, tb, tc, tt, tu;
-  int rc;
-  if ((rc = make_tmap_bf16_chunks(&ta, A, p.K, p.M, 1, a_rows, lt.kch))) return rc;
-  if ((rc = make_tmap_bf16_chunks(&tb, W, p.K, p.N, 1, BN, lt.kch))) return rc;
+  int rc, a_rows = BM;
+  if constexpr (WIDE) {
+    // Rows past M would be zero-filled; the accumulator rows that other shared memory gives instead are not
+    // stored (the MMA reads 128 rows from each chunk on, which ends inside the ring or the epilogue's boxes).
+    if (p.M < BM) a_rows = (p.M + 7) / 8 * 8;
+    lt.a_pitch = a_rows * BK * 2;
+    // One row tile streams W once, and a stage's turn (a wait, a load of A and one of W by one thread) takes
+    // about 0.3 us whatever it loads: as many K steps a stage as leave three stages. 6144 x 6144 by one row:
+    // 34 us with one K step a stage, 17 us with four.
+    const int step = lt.a_pitch + Cfg::B_BYTES, ring = Cfg::STAGES * Cfg::STAGE_BYTES;
+    lt.kch = 12 * step <= ring ? 4 : 6 * step <= ring ? 2 : 1;
+    lt.stage_bytes = lt.kch * step;
+    lt.stages = ring / lt.stage_bytes;
+    if (lt.stages > MAX_STAGES) lt.stages = MAX_STAGES;
+    if ((rc = make_tmap_bf16_chunks(&ta, A, p.K, p.M, 1, a_rows, lt.kch))) return rc;
+    if ((rc = make_tmap_bf16_chunks(&tb, W, p.K, p.N, 1, BN, lt.kch))) return rc;
+  } else {
+    if ((rc = make_tmap_bf16_2d(&ta, A, p.K, p.M, p.K, BK, BM))) return rc;
+    if ((rc = make_tmap_bf16_2d(&tb, W, p.K, p.N, p.K, BK, BN))) return rc;
+  }
   if ((rc = make_tmap_bf16_2d(&tt, t, 2 * lt.rankp, (uint64_t)lora_units(p.M, l.R) * BM, 2 * lt.rankp, 64, a_rows)))
     return rc;
   if ((rc = make_tmap_bf16_3d(&tu, l.up, l.rank, p.N, l.n_adapters, l.rank, 64, BN, p.N))) return rc;
@@ -792,23 +796,29 @@ int gemm_bf16_lora(int epi, const GemmParams& p, const void* A, const void* W, c
   const int sms = num_sms();
   const long tm = (p.M + BM - 1) / BM;
   const double e128 = wave_eff(tm * (p.N / 128), sms);
-  int bn = 128;
-  if (p.N % 256 == 0 && (wave_eff(tm * (p.N / 256), sms) >= 0.8 * e128 || tm * (p.N / 256) >= 4L * sms)) bn = 256;
-  // few tiles: narrower ones put more SMs on the stream of W (a SwiGLU tile is 128 columns at least)
-  if (bn == 128 && epi != EPI_SWIGLU && wave_eff(tm * (p.N / 64), sms) > 1.25 * e128) bn = 64;
-#define KREA2_GEMM_LORA(E)                                                              \
-  return bn == 256 ? launch_gemm_lora_bn<256, E>(p, A, W, l, t, stream)                 \
-                   : launch_gemm_lora_bn<128, E>(p, A, W, l, t, stream)
-  switch (epi) {
-    case EPI_STORE:
-      if (bn == 64) return launch_gemm_lora_bn<64, EPI_STORE>(p, A, W, l, t, stream);
-      KREA2_GEMM_LORA(EPI_STORE);
-    case EPI_SWIGLU: KREA2_GEMM_LORA(EPI_SWIGLU);
-    default:
-      if (bn == 64) return launch_gemm_lora_bn<64, EPI_RESID>(p, A, W, l, t, stream);
-      KREA2_GEMM_LORA(EPI_RESID);
+  if (tm == 1) {
+    // few tiles: narrower ones put more SMs on the stream of W (a SwiGLU tile is 128 columns at least)
+    const bool narrow = wave_eff(p.N / 64, sms) > 1.25 * e128;
+    if (epi == EPI_SWIGLU) return launch_gemm_lora_bn<128, EPI_SWIGLU, true>(p, A, W, l, t, stream);
+    if (epi == EPI_STORE)
+      return narrow ? launch_gemm_lora_bn<64, EPI_STORE, true>(p, A, W, l, t, stream)
+                    : launch_gemm_lora_bn<128, EPI_STORE, true>(p, A, W, l, t, stream);
+    return narrow ? launch_gemm_lora_bn<64, EPI_RESID, true>(p, A, W, l, t, stream)
+                  : launch_gemm_lora_bn<128, EPI_RESID, true>(p, A, W, l, t, stream);
   }
-#undef KREA2_GEMM_LORA
+  const long t256 = tm * (p.N / 256);
+  if (p.N % 256 == 0 && (wave_eff(t256, sms) >= 0.8 * e128 || t256 >= 4L * sms)) {
+    switch (epi) {
+      case EPI_STORE: return launch_gemm_lora_bn<256, EPI_STORE, false>(p, A, W, l, t, stream);
+      case EPI_SWIGLU: return launch_gemm_lora_bn<256, EPI_SWIGLU, false>(p, A, W, l, t, stream);
+      default: return launch_gemm_lora_bn<256, EPI_RESID, false>(p, A, W, l, t, stream);
+    }
+  }
+  switch (epi) {
+    case EPI_STORE: return launch_gemm_lora_bn<128, EPI_STORE, false>(p, A, W, l, t, stream);
+    case EPI_SWIGLU: return launch_gemm_lora_bn<128, EPI_SWIGLU, false>(p, A, W, l, t, stream);
+    default: return launch_gemm_lora_bn<128, EPI_RESID, false>(p, A, W, l, t, stream);
+  }
 }
 
 }  // namespace krea2
