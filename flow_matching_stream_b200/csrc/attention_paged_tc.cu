@@ -1,0 +1,791 @@
+// Attention of a ragged batch's new tokens over a paged key/value cache on the sm_100a tensor cores:
+//   out = sigmoid(g) softmax(q_hat k_hatᵀ / sqrt(D)) v,  q_hat = RoPE(q / rms(q) (1 + w)),
+// one pass over the keys with the running maximum and sum of each row's softmax.
+//
+// Bound: the tensor cores and the exponentials for many new tokens (4 D H operations a token and key),
+// reading K and V once (512 bytes a key and KV head) for few.
+//
+// An item is (request, KV head, 128 / G new tokens): its 128 MMA rows are G query heads of 128 / G
+// tokens, row = token * G + head, so that few tokens fill whole warps and leave the others idle. Work is
+// cut into key tiles of 64. Every CTA (two per SM, all resident) takes
+//   * whole items in turn, as many rounds as every CTA gets one item of a request: neighbours work on
+//     the same K and V at the same time;
+//   * an equal share of the key tiles of what is left, cut without regard to items. A cut item's parts
+//     (unnormalised O, row maximum and sum, fp32) go to the workspace, and a second kernel joins them in
+//     key order. One new token over a long cache is spread over all SMs this way.
+//
+// Roles as in attention_tc.cu, but the CTA runs through segments (an item or a part of one):
+//   warp 0      cuts the work into segments and publishes them, looks up pages, loads K and V tiles by
+//               TMA, one box per page and tile (per 16, 32 or 64 keys), into a 2-stage ring
+//   warp 1      S = Q Kᵀ into one of two TMEM buffers, O += P V with P in TMEM
+//   warps 2..9  normalise and rotate a segment's queries into shared memory, softmax, output. Where keys
+//               of a tile are masked or lie behind the request's last key, they clear those rows of V in
+//               shared memory, so that whatever the page holds there meets no probability of zero.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "attention_device.cuh"
+#include "krea2_device.cuh"
+#include "krea2_internal.h"
+#include "ragged.cuh"
+
+namespace krea2 {
+
+KREA2_DEFINE_ERROR_READER(take_device_error_paged_tc)
+
+namespace {
+
+constexpr int KT = 64;            // keys per tile
+constexpr int KV_STAGES = 2;
+constexpr int THREADS = 320;
+constexpr int SOFTMAX_THREADS = 256;
+constexpr int Q_CHUNK = 128 * 128;  // 128 rows x 64 bf16
+constexpr int KV_CHUNK = KT * 128;  // 64 keys x 64 bf16
+constexpr int KV_TILE_BYTES = 2 * KV_CHUNK;
+constexpr int OFF_K = 2 * Q_CHUNK;
+constexpr int OFF_V = OFF_K + KV_STAGES * KV_TILE_BYTES;
+constexpr int SMEM_BYTES = OFF_V + KV_STAGES * KV_TILE_BYTES + 1024;
+constexpr uint32_t TMEM_COLS = 256;  // S0 [0,64), S1 [64,128), O [128,256)
+constexpr uint32_t O_COL = 128;
+constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, KT, 0, 0);
+constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, AD, 0, 1);
+constexpr int MIN_SHARE = 4;         // key tiles: below that a CTA's start costs more than it shares
+constexpr int TILE_RING = 8;         // tile numbers in flight between warp 0 and the softmax warps
+
+struct Args {
+  PagedArgs b;
+  int H, Hkv, T;
+  float eps, scale_log2;
+  const __nv_bfloat16* qkvg;
+  const float* qw;
+  const float* cos;
+  const float* sin;
+  const uint8_t* text_mask;
+  const int32_t* key_end;
+  __nv_bfloat16* out;
+  float* part_o;   // (2 CTAs, part_rows, 128)
+  float* part_ml;  // (2 CTAs, part_rows, 2): maximum in powers of two, sum
+  int part_rows;
+  int group;       // keys per TMA box: 16, 32 or 64, a divisor of the page size
+  int split;       // items may be cut
+  int ctas;
+};
+
+struct ItemPlan {
+  RequestRows q;
+  int tiles, qtiles, rounds, rest;  // rest: items beyond the whole rounds
+  long long weight;                 // of the rest, in tiles (in items where items are not cut)
+};
+
+template <int G>
+__device__ __forceinline__ ItemPlan plan_of(const Args& a, int r, bool* bad) {
+  constexpr int QPOS = 128 / G;
+  ItemPlan p;
+  *bad = !request_rows(r, a.b.M, (long long)a.b.max_pages * a.b.page_size, a.b.q_start, a.b.kv_len, &p.q);
+  if (*bad) p.q.n = 0;
+  p.tiles = p.q.n ? (p.q.L + KT - 1) / KT : 1;
+  p.qtiles = (p.q.n + QPOS - 1) / QPOS;
+  const long long items = (long long)p.qtiles * a.Hkv;
+  p.rounds = (int)(items / a.ctas);
+  p.rest = (int)(items % a.ctas);
+  p.weight = (long long)p.rest * (a.split ? p.tiles : 1);
+  return p;
+}
+
+// The batch's shared work (every request's rest, in order) and the place `part * share` in it. All threads
+// of the block call it.
+struct Place {
+  long long total, share, offset;  // offset: within request r's weight
+  int r;                           // a.b.R: the place is behind the end
+  int rounds;                      // whether a request has whole rounds
+};
+template <int G>
+__device__ Place find_place(const Args& a, int part, Place* shared, long long* warp_sums) {
+  const int tid = threadIdx.x, nt = blockDim.x, warp = tid >> 5, lane = tid & 31;
+  const int per = (a.b.R + nt - 1) / nt, r0 = min(tid * per, a.b.R), r1 = min(r0 + per, a.b.R);
+  long long sum = 0;
+  int rounds = 0;
+  for (int r = r0; r < r1; ++r) {
+    bool bad;
+    const ItemPlan p = plan_of<G>(a, r, &bad);
+    if (bad && blockIdx.x == 0) atomicOr(&g_device_error, ERR_BAD_BATCH);
+    sum += p.weight;
+    rounds |= p.rounds;
+  }
+  long long incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) warp_sums[warp] = incl;
+  if (tid == 0) shared->r = a.b.R;
+  rounds = __syncthreads_or(rounds);
+  long long before = 0, total = 0;
+  for (int w = 0; w < nt / 32; ++w) {
+    if (w < warp) before += warp_sums[w];
+    total += warp_sums[w];
+  }
+  long long share = (total + a.ctas - 1) / a.ctas;
+  if (a.split && share < MIN_SHARE) share = MIN_SHARE;
+  if (share < 1) share = 1;
+  const long long at = part * share, lo = before + incl - sum;
+  if (at >= lo && at < lo + sum) {  // one thread at most
+    long long left = at - lo;
+    for (int r = r0; r < r1; ++r) {
+      bool bad;
+      const ItemPlan p = plan_of<G>(a, r, &bad);
+      if (left < p.weight) {
+        shared->r = r;
+        shared->offset = left;
+        break;
+      }
+      left -= p.weight;
+    }
+  }
+  __syncthreads();
+  Place x = *shared;
+  x.total = total;
+  x.share = share;
+  x.rounds = rounds;
+  return x;
+}
+
+// What the roles know of a segment.
+struct Segment {
+  int row0, n;        // packed row of its first token, tokens (n < 0: no more segments)
+  int r, L, pos0;     // request, its keys, the first token's position
+  int j;              // KV head
+  int tiles;          // key tiles that are computed (tiles of masked keys are left out)
+  int kmin;           // keys below it need no per-row limit
+  int slot;           // part number, or -1: the whole item
+};
+
+__device__ __forceinline__ bool key_used(const Args& a, int r, int L, int t) {
+  if (t >= L) return false;
+  return !(a.text_mask && t < a.T) || a.text_mask[(long long)r * a.T + t] != 0;
+}
+
+// Whether each of 32 tiles from t0 on (one per lane) has a key to compute.
+__device__ __forceinline__ uint32_t used_tiles(const Args& a, int r, int L, int t0, int t1, int lane) {
+  const int t = t0 + lane;
+  bool used = false;
+  if (t < t1) {
+    const int k0 = t * KT, k1 = min(k0 + KT, L);
+    used = !a.text_mask || k1 > a.T;
+    for (int k = k0; k < k1 && !used; ++k) used = a.text_mask[(long long)r * a.T + k] != 0;
+  }
+  return __ballot_sync(0xffffffffu, used);
+}
+
+template <int G>
+__global__ void __launch_bounds__(THREADS, 2)
+    paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, Args a) {
+  constexpr int QPOS = 128 / G;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t seg_full[2], seg_empty[2];
+  __shared__ __align__(8) uint64_t q_full;
+  __shared__ __align__(8) uint64_t k_full[KV_STAGES], k_empty[KV_STAGES], v_full[KV_STAGES], v_empty[KV_STAGES];
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done[2];
+  __shared__ __align__(8) uint64_t drain_bar;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ Segment segs[2];
+  __shared__ int tile_of[TILE_RING];
+  __shared__ Place place_sh;
+  __shared__ long long warp_sums[THREADS / 32];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t base_u32 = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* base = smem_raw + (base_u32 - smem_u32(smem_raw));
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&seg_full[s], 1);
+      mbar_init(&seg_empty[s], SOFTMAX_THREADS + 1);
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], SOFTMAX_THREADS);
+      mbar_init(&pv_done[s], 1);
+    }
+    mbar_init(&q_full, SOFTMAX_THREADS);
+    mbar_init(&drain_bar, 1);
+    abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 1) tmem_alloc(&tmem_slot, TMEM_COLS);
+  const Place place = find_place<G>(a, blockIdx.x, &place_sh, warp_sums);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  volatile int* abort = &abort_flag;
+
+  if (warp == 0) {
+    // ---- segments and K/V loads. The whole warp runs along; lane 0 signs for the bytes, lanes issue boxes.
+    int it = 0, seg = 0;  // tiles and segments so far
+    IssuedFills k_fills, v_fills;
+    const int per_page = a.b.page_size / a.group, boxes = KT / a.group;
+    bool ok = true;
+
+    auto publish = [&](const Segment& s) -> bool {
+      if (!__all_sync(0xffffffffu, mbar_wait(&seg_empty[seg & 1], ((seg >> 1) & 1) ^ 1, abort))) return false;
+      if (lane == 0) {
+        segs[seg & 1] = s;
+        mbar_arrive(&seg_full[seg & 1]);
+      }
+      ++seg;
+      return true;
+    };
+    // One item (or the tiles [t0, t1) of it): the segment, then its tiles.
+    auto run_item = [&](const ItemPlan& p, int r, int item, int t0, int t1, int slot) -> bool {
+      Segment s;
+      const int qt = item % p.qtiles;
+      s.j = item / p.qtiles;
+      s.r = r;
+      s.L = p.q.L;
+      s.row0 = p.q.row0 + qt * QPOS;
+      s.n = min(QPOS, p.q.n - qt * QPOS);
+      s.pos0 = p.q.L - p.q.n + qt * QPOS;
+      s.slot = slot;
+      s.kmin = p.q.L;
+      int te = t1;
+      if (a.key_end) {
+        int hi = 0, lo = p.q.L;
+        for (int i = lane; i < s.n; i += 32) {
+          const int e = min(max(a.key_end[s.row0 + i], s.pos0 + i + 1), p.q.L);
+          hi = max(hi, e);
+          lo = min(lo, e);
+        }
+        s.kmin = __reduce_min_sync(0xffffffffu, lo);
+        te = min(te, (__reduce_max_sync(0xffffffffu, hi) + KT - 1) / KT);
+      }
+      s.tiles = max(te - t0, 0);
+      const int text_tiles = a.text_mask ? min(te, a.T / KT) : 0;  // tiles that may hold masked keys only
+      for (int t = t0; t < text_tiles; t += 32)
+        s.tiles -= min(32, text_tiles - t) - __popc(used_tiles(a, r, p.q.L, t, text_tiles, lane));
+      if (!publish(s)) return false;
+
+      const int32_t* pages = a.b.page_table + (long long)r * a.b.max_pages;
+      const int groups = (p.q.L + a.group - 1) / a.group;  // boxes that hold keys
+      uint32_t used = 0;
+      int my_page = 0, my_slot = 0, cached = -1;  // lane i: page and slot of box cached + i
+      int prev_tile = -1;                          // the tile whose V is still to be loaded
+      int prev_page = 0, prev_slot = 0;
+      bool prev_has = false;
+      int prev_count = 0;
+      auto load_v = [&]() -> bool {
+        const int i = it - 1, st = i & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(&v_empty[st], ((i >> 1) & 1) ^ 1, abort))) return false;
+        uint8_t* vd = base + OFF_V + st * KV_TILE_BYTES;
+        if (lane == 0) mbar_arrive_expect_tx(&v_full[st], prev_count * a.group * (2 * AD));
+        __syncwarp();
+        if (a.group == KT) {
+          if (lane == 0) tma_load_4d(vd, &tmV, &v_full[st], 0, prev_slot, s.j * 2, prev_page);
+        } else if (prev_has) {
+          tma_load_4d(vd + (lane & 1) * KV_CHUNK + (lane >> 1) * a.group * 128, &tmV, &v_full[st], 0, prev_slot,
+                      s.j * 2 + (lane & 1), prev_page);
+        }
+        v_fills.note(st, (i >> 1) & 1);
+        return true;
+      };
+      for (int t = t0; t < te; ++t) {
+        if (t < text_tiles) {
+          if (t == t0 || (t - t0) % 32 == 0) used = used_tiles(a, r, p.q.L, t, text_tiles, lane);
+          if (!((used >> ((t - t0) & 31)) & 1u)) continue;
+        }
+        // pages of the tile's boxes: 32 boxes looked up at once
+        const int g0 = t * boxes;
+        if (cached < 0 || g0 + boxes > cached + 32) {
+          cached = g0;
+          const int g = g0 + lane;
+          my_page = a.b.num_pages;  // outside the pool: reads as zeros
+          my_slot = 0;
+          if (g < groups) {
+            const int pg = pages[g / per_page];
+            my_slot = (g % per_page) * a.group;
+            if (pg >= 0 && pg < a.b.num_pages) my_page = pg;
+            else atomicOr(&g_device_error, ERR_BAD_BATCH);
+          }
+        }
+        const int count = min(boxes, groups - g0);
+        // lane 2 b + c: box b, 64-column chunk c (one box per tile: both chunks at once, by lane 0)
+        const int src = min(g0 - cached + (a.group == KT ? 0 : lane >> 1), 31);
+        const int page = __shfl_sync(0xffffffffu, my_page, src), slot_in = __shfl_sync(0xffffffffu, my_slot, src);
+        const bool has = (lane >> 1) < count;
+        const int st = it & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(&k_empty[st], ((it >> 1) & 1) ^ 1, abort))) return false;
+        uint8_t* kd = base + OFF_K + st * KV_TILE_BYTES;
+        if (lane == 0) {
+          tile_of[it % TILE_RING] = t;
+          mbar_arrive_expect_tx(&k_full[st], count * a.group * (2 * AD));
+        }
+        __syncwarp();
+        if (a.group == KT) {
+          if (lane == 0) tma_load_4d(kd, &tmK, &k_full[st], 0, slot_in, s.j * 2, page);
+        } else if (has) {
+          tma_load_4d(kd + (lane & 1) * KV_CHUNK + (lane >> 1) * a.group * 128, &tmK, &k_full[st], 0, slot_in,
+                      s.j * 2 + (lane & 1), page);
+        }
+        k_fills.note(st, (it >> 1) & 1);
+        // V runs one tile behind K: V stages free up after P V only
+        if (prev_tile >= 0 && !load_v()) return false;
+        ++it;
+        prev_tile = t;
+        prev_page = page;
+        prev_slot = slot_in;
+        prev_has = has;
+        prev_count = count;
+      }
+      return prev_tile < 0 || load_v();
+    };
+
+    if (place.rounds)
+      for (int r = 0; r < a.b.R && ok; ++r) {
+        bool bad;
+        const ItemPlan p = plan_of<G>(a, r, &bad);
+        for (int k = 0; k < p.rounds && ok; ++k) ok = run_item(p, r, k * a.ctas + blockIdx.x, 0, p.tiles, -1);
+      }
+    long long left = min(place.share, place.total - blockIdx.x * place.share), off = place.offset;
+    for (int r = place.r; r < a.b.R && left > 0 && ok; ++r, off = 0) {
+      bool bad;
+      const ItemPlan p = plan_of<G>(a, r, &bad);
+      const int unit = a.split ? p.tiles : 1;  // weight of an item
+      while (off < p.weight && left > 0 && ok) {
+        const int item = p.rounds * a.ctas + (int)(off / unit), from = (int)(off % unit);
+        const int len = (int)min((long long)(unit - from), left);
+        // a part that does not start its item is the CTA's first, one that does not end it its last
+        const int slot = len == unit ? -1 : 2 * blockIdx.x + (from == 0 ? 1 : 0);
+        ok = a.split ? run_item(p, r, item, from, from + len, slot) : run_item(p, r, item, 0, p.tiles, -1);
+        off += len;
+        left -= len;
+      }
+    }
+    if (ok) {
+      Segment end{};
+      end.n = -1;
+      publish(end);
+    }
+    if (*abort && lane == 0) {
+      k_fills.drain(k_full, KV_STAGES);
+      v_fills.drain(v_full, KV_STAGES);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint64_t dq0 = smem_desc_sw128(smem_u32(base), 16, 1024);
+      const uint64_t dk0 = smem_desc_sw128(smem_u32(base + OFF_K), 16, 1024);
+      const uint64_t dv0 = smem_desc_sw128(smem_u32(base + OFF_V), KV_CHUNK, 1024);
+      bool issued = false, ok = true;
+      int it = 0;
+      int queries = 0;  // segments with tiles so far
+      for (int seg = 0; ok; ++seg) {
+        if (!mbar_wait(&seg_full[seg & 1], (seg >> 1) & 1, abort)) break;
+        const int n = segs[seg & 1].n, tiles = segs[seg & 1].tiles;
+        mbar_arrive(&seg_empty[seg & 1]);
+        if (n < 0) break;
+        if (tiles == 0) continue;  // no product, and no arrival on q_full
+        if (!mbar_wait(&q_full, queries++ & 1, abort)) break;
+        tc_fence_after();
+        const int first = it;
+        auto issue_pv = [&](int i) -> bool {
+          const int st = i & 1;
+          if (!mbar_wait2(&p_full[st], (i >> 1) & 1, &v_full[st], (i >> 1) & 1, abort)) return false;
+          tc_fence_after();
+          const uint64_t dv = dv0 + (uint64_t)(st * (KV_TILE_BYTES >> 4));
+          const uint32_t pt = tmem + st * KT;
+#pragma unroll
+          for (int kk = 0; kk < KT / 16; ++kk)
+            tc_mma_bf16_ts(tmem + O_COL, pt + kk * 8, dv + (uint64_t)(kk * 16 * 128 >> 4), IDESC_PV,
+                           (i > first || kk > 0) ? 1u : 0u);
+          tc_commit(&pv_done[st]);
+          tc_commit(&v_empty[st]);
+          return true;
+        };
+        for (int i = 0; i < tiles; ++i, ++it) {
+          const int st = it & 1;
+          if (!mbar_wait(&k_full[st], (it >> 1) & 1, abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t dk = dk0 + (uint64_t)(st * (KV_TILE_BYTES >> 4));
+          const uint32_t d_s = tmem + st * KT;
+#pragma unroll
+          for (int kk = 0; kk < AD / 16; ++kk) {
+            const uint32_t qo = (kk >> 2) * Q_CHUNK + (kk & 3) * 32;
+            const uint32_t ko = (kk >> 2) * KV_CHUNK + (kk & 3) * 32;
+            tc_mma_bf16(d_s, dq0 + (uint64_t)(qo >> 4), dk + (uint64_t)(ko >> 4), IDESC_QK, kk > 0 ? 1u : 0u);
+          }
+          issued = true;
+          tc_commit(&s_full[st]);
+          tc_commit(&k_empty[st]);
+          if (i >= 1 && !issue_pv(it - 1)) {
+            ok = false;
+            break;
+          }
+        }
+        if (ok) ok = issue_pv(it - 1);
+      }
+      if (*abort && issued) {
+        tc_commit(&drain_bar);
+        mbar_wait_drain(&drain_bar, 0);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---- queries, softmax and output: warps w and w + 4 share TMEM lane quarter w & 3, 16 rows each;
+    // threads t and t + 16 hold the same row and split its 64 scores and 128 output columns
+    const int quarter = warp & 3, sub = (warp - 2) >> 2, half = lane >> 4;
+    const int warp_row = quarter * 32 + sub * 16;
+    const int row = warp_row + (lane & 15);
+    const uint32_t lane_off = (uint32_t)warp_row << 16;
+    const float sl2 = a.scale_log2;
+    const long long qc = 2LL * (a.H + a.Hkv) * AD;
+    constexpr int HK = KT / 2;
+    int it = 0, seg = 0;
+    Segment s;
+    // Segment's queries, normalised and rotated, into shared memory (row = token * G + head, 128-byte swizzle)
+    auto next_segment = [&]() -> bool {
+      if (!__all_sync(0xffffffffu, mbar_wait(&seg_full[seg & 1], (seg >> 1) & 1, abort))) return false;
+      s = segs[seg & 1];
+      if (s.n < 0) return false;
+      // without tiles there is nothing to wait for on the other side, so q_full must not advance either: the
+      // phase of a later segment could complete before the MMA thread has seen this one
+      if (s.tiles == 0) return true;
+      const float4 w4 = *reinterpret_cast<const float4*>(a.qw + lane * 4);
+      const int rows = min(16, s.n * G - warp_row);
+#pragma unroll 1
+      for (int i0 = 0; i0 < rows; i0 += 4) {
+        uint2 raw[4];
+        float2 c[4], sn[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = warp_row + min(i0 + i, rows - 1), prow = s.row0 + rr / G;
+          raw[i] = *reinterpret_cast<const uint2*>(a.qkvg + prow * qc + (s.j * G + rr % G) * AD + lane * 4);
+          c[i] = *reinterpret_cast<const float2*>(a.cos + (long long)prow * (AD / 2) + lane * 2);
+          sn[i] = *reinterpret_cast<const float2*>(a.sin + (long long)prow * (AD / 2) + lane * 2);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = warp_row + min(i0 + i, rows - 1);
+          float v[4] = {bf16_lo(raw[i].x), bf16_hi(raw[i].x), bf16_lo(raw[i].y), bf16_hi(raw[i].y)};
+          const float ss = warp_sum(v[0] * v[0] + v[1] * v[1] + v[2] * v[2] + v[3] * v[3]);
+          const float rs = rsqrtf(ss / (float)AD + a.eps);
+          v[0] *= rs * (1.f + w4.x);
+          v[1] *= rs * (1.f + w4.y);
+          v[2] *= rs * (1.f + w4.z);
+          v[3] *= rs * (1.f + w4.w);
+          uint2 o;
+          o.x = pack_bf16x2(v[0] * c[i].x - v[1] * sn[i].x, v[1] * c[i].x + v[0] * sn[i].x);
+          o.y = pack_bf16x2(v[2] * c[i].y - v[3] * sn[i].y, v[3] * c[i].y + v[2] * sn[i].y);
+          *reinterpret_cast<uint2*>(base + (lane >> 4) * Q_CHUNK + rr * 128 + ((((lane & 15) >> 1) ^ (rr & 7)) << 4) +
+                                    (lane & 1) * 8) = o;
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&q_full);
+      return true;
+    };
+
+    bool ok = next_segment();
+    while (ok) {
+      const Segment cur = s;
+      const bool active = warp_row < cur.n * G;  // the warp holds rows of the segment
+      const int tok = row / G;
+      int row_kend = cur.L;
+      if (a.key_end && tok < cur.n) row_kend = min(max(a.key_end[cur.row0 + tok], cur.pos0 + tok + 1), cur.L);
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; i < cur.tiles; ++i, ++it) {
+        const int sb = it & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[sb], (it >> 1) & 1, abort))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int t0 = tile_of[it % TILE_RING] * KT;
+        const uint32_t sbase = tmem + lane_off + sb * KT;
+        uint32_t vm0 = 0xffffffffu, vm1 = 0xffffffffu;
+        if ((a.text_mask && t0 < a.T) || t0 + KT > cur.L) {
+          vm0 = __ballot_sync(0xffffffffu, key_used(a, cur.r, cur.L, t0 + lane));
+          vm1 = __ballot_sync(0xffffffffu, key_used(a, cur.r, cur.L, t0 + 32 + lane));
+          if ((vm0 & vm1) != 0xffffffffu) {  // the same for all warps: clear the V rows of unused keys
+            if (!__all_sync(0xffffffffu, mbar_wait(&v_full[sb], (it >> 1) & 1, abort))) {
+              ok = false;
+              break;
+            }
+            const int key = (threadIdx.x - 64) >> 2, part = threadIdx.x & 3;
+            const uint32_t vm = key < 32 ? vm0 : vm1;
+            if (!((vm >> (key & 31)) & 1u)) {
+              uint8_t* v = base + OFF_V + sb * KV_TILE_BYTES + (part >> 1) * KV_CHUNK + key * 128 + (part & 1) * 64;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) reinterpret_cast<uint4*>(v)[q] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+          }
+        }
+        if (active) {
+          float v[HK];
+          tmem_ld32_pair<HK>(sbase, v);
+          const uint32_t vm = half ? vm1 : vm0;
+          if ((vm0 & vm1) != 0xffffffffu) {
+#pragma unroll
+            for (int e = 0; e < HK; ++e)
+              if (!((vm >> e) & 1u)) v[e] = -INFINITY;
+          }
+          if (t0 + KT > cur.kmin) {
+            const int lim = row_kend - (t0 + half * HK);
+#pragma unroll
+            for (int e = 0; e < HK; ++e)
+              if (e >= lim) v[e] = -INFINITY;
+          }
+          float m4[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float x = v[k];
+#pragma unroll
+            for (int t = 1; t < 7; t += 2) x = fmax3(x, v[k + 4 * t], v[k + 4 * t + 4]);
+            m4[k] = fmaxf(x, v[k + 28]);
+          }
+          const float hm = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          const float mx = fmaxf(hm, __shfl_xor_sync(0xffffffffu, hm, 16));
+          const float mnew = fmaxf(m, mx * sl2);
+          const bool grow = mnew > m + 8.0f;  // m = -inf on the first tile
+          float alpha = 1.f;
+          const bool any_grow = __any_sync(0xffffffffu, grow);
+          if (grow) {
+            alpha = ex2(m - mnew);  // 0 on the first tile
+            m = mnew;
+          }
+          uint32_t pk[HK / 2];
+          const float rs = exp_tile<HK>(v, sl2, m == -INFINITY ? 0.f : m, pk);
+          l = l * alpha + rs;
+          tmem_st16_pair<HK / 2>(sbase, pk);
+          if (i >= 1 && any_grow) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, abort))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < AD / 64; ++c) {
+              float o[32];
+              const uint32_t oa = tmem + lane_off + O_COL + c * 32;
+              tmem_ld32_pair<AD / 2>(oa, o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= alpha;
+              tmem_st32_pair<AD / 2>(oa, o);
+            }
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(&p_full[sb]);
+      }
+      if (!ok) break;
+      // the last s_full was the last use of Q: the next segment's queries go in, and its first product
+      // starts while this segment's output is written
+      ++seg;
+      const bool more = next_segment();
+      if (cur.tiles > 0) {
+        const int i = it - 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[i & 1], (i >> 1) & 1, abort))) break;
+        tc_fence_after();
+      }
+      if (active) {
+        const float lt = l + __shfl_xor_sync(0xffffffffu, l, 16);
+        const bool row_ok = tok < cur.n;
+        const float inv_l = lt > 0.f ? 1.f / lt : (lt == 0.f ? 0.f : lt);  // no readable key: zeros; NaN stays
+        const int h = cur.j * G + row % G;
+        const long long prow = cur.row0 + tok;
+#pragma unroll 1
+        for (int c = 0; c < AD / 64; ++c) {
+          const int col = half * (AD / 2) + c * 32;
+          float o[32];
+          if (cur.tiles > 0) {
+            tmem_ld32_pair<AD / 2>(tmem + lane_off + O_COL + c * 32, o);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          }
+          if (row_ok && cur.slot >= 0) {
+            float4* po = reinterpret_cast<float4*>(a.part_o + ((long long)cur.slot * a.part_rows + row) * AD + col);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) po[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          } else if (row_ok) {
+            const uint4* gp = reinterpret_cast<const uint4*>(a.qkvg + prow * qc + (a.H + 2 * a.Hkv + h) * AD + col);
+            uint4* op = reinterpret_cast<uint4*>(a.out + prow * (a.H * AD) + h * AD + col);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint4 gv = __ldg(gp + q);
+              const uint32_t gw[4] = {gv.x, gv.y, gv.z, gv.w};
+              uint32_t ow[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                ow[e] = pack_bf16x2(o[q * 8 + 2 * e] * inv_l * sigmoid_f(bf16_lo(gw[e])),
+                                    o[q * 8 + 2 * e + 1] * inv_l * sigmoid_f(bf16_hi(gw[e])));
+              op[q] = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+            }
+          }
+          __syncwarp();
+        }
+        if (cur.slot >= 0 && row_ok && half == 0) {
+          float2* ml = reinterpret_cast<float2*>(a.part_ml) + (long long)cur.slot * a.part_rows + row;
+          *ml = make_float2(m, lt);
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&seg_empty[(seg - 1) & 1]);
+      ok = more;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+// Joins the parts of cut items: block c looks at the place where CTA c's share starts, and joins the item
+// that is cut there if no earlier place cuts it. Parts come in key order, so results repeat bit for bit.
+template <int G>
+__global__ void __launch_bounds__(256) paged_attn_join_kernel(Args a) {
+  constexpr int QPOS = 128 / G;
+  __shared__ Place place_sh;
+  __shared__ long long warp_sums[8];
+  const int c = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Place place = find_place<G>(a, c, &place_sh, warp_sums);
+  if (place.r >= a.b.R) return;
+  bool bad;
+  const ItemPlan p = plan_of<G>(a, place.r, &bad);
+  const int within = (int)(place.offset % p.tiles);
+  if (within == 0) return;  // the share starts with an item
+  const long long start = (long long)c * place.share - within;
+  if (start / place.share + 1 != c) return;
+  const int last = (int)((start + p.tiles - 1) / place.share);
+  const int item = p.rounds * a.ctas + (int)(place.offset / p.tiles);
+  const int qt = item % p.qtiles, j = item / p.qtiles;
+  const int rows = min(QPOS, p.q.n - qt * QPOS) * G;
+  const long long qc = 2LL * (a.H + a.Hkv) * AD;
+  for (int row = warp; row < rows; row += 8) {
+    const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + row;
+    auto slot_of = [&](int k) { return (long long)(k < c ? 2 * (c - 1) + 1 : 2 * k) * a.part_rows; };
+    float top = -INFINITY;
+    for (int k = c - 1; k <= last; ++k) top = fmaxf(top, ml[slot_of(k)].x);
+    float o[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
+    for (int k = c - 1; k <= last; ++k) {
+      const float2 v = ml[slot_of(k)];
+      if (v.x == -INFINITY && v.y == 0.f) continue;  // no readable key in this part
+      const float w = ex2(v.x - top);
+      const float4 x = *reinterpret_cast<const float4*>(a.part_o + (slot_of(k) + row) * AD + lane * 4);
+      sum += w * v.y;
+      o[0] += w * x.x;
+      o[1] += w * x.y;
+      o[2] += w * x.z;
+      o[3] += w * x.w;
+    }
+    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+    const int h = j * G + row % G;
+    const long long prow = p.q.row0 + qt * QPOS + row / G;
+    const uint2 g = *reinterpret_cast<const uint2*>(a.qkvg + prow * qc + (a.H + 2 * a.Hkv + h) * AD + lane * 4);
+    uint2 r;
+    r.x = pack_bf16x2(o[0] * inv * sigmoid_f(bf16_lo(g.x)), o[1] * inv * sigmoid_f(bf16_hi(g.x)));
+    r.y = pack_bf16x2(o[2] * inv * sigmoid_f(bf16_lo(g.y)), o[3] * inv * sigmoid_f(bf16_hi(g.y)));
+    *reinterpret_cast<uint2*>(a.out + prow * (a.H * AD) + h * AD + lane * 4) = r;
+  }
+}
+
+int make_tmap_pages(CUtensorMap* m, const void* ptr, int Hkv, const Krea2PagedBatch& b, int group) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tmap_encoder();
+  if (!enc) return set_error(KREA2_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  const cuuint64_t row = (cuuint64_t)Hkv * AD * 2;
+  cuuint64_t dims[4] = {64, (cuuint64_t)b.page_size, (cuuint64_t)Hkv * 2, (cuuint64_t)b.num_pages};
+  cuuint64_t strides[3] = {row, 128, row * b.page_size};
+  // both 64-column chunks of a head at once where a box is a whole tile
+  cuuint32_t box[4] = {64, (cuuint32_t)group, group == KT ? 2u : 1u, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(KREA2_ERR_CUDA, "cuTensorMapEncodeTiled (pages) failed (%d)", (int)r);
+  return KREA2_OK;
+}
+
+// Launch sizes from what the host knows: row and request counts and the longest sequence the table holds.
+struct Shape {
+  int ctas, split, part_rows;
+};
+Shape shape_of(const Krea2PagedBatch& b, int H, int Hkv) {
+  const int G = H / Hkv, qpos = 128 / G;
+  const long long qtiles = b.M < b.M / qpos + b.R ? b.M : b.M / qpos + (long long)b.R;
+  const long long tiles = ((long long)b.max_pages * b.page_size + KT - 1) / KT;
+  Shape s;
+  s.split = tiles > MIN_SHARE;
+  const long long most = qtiles * Hkv * (s.split ? (tiles + MIN_SHARE - 1) / MIN_SHARE : 1);
+  s.ctas = (int)(most < 2LL * num_sms() ? most : 2LL * num_sms());
+  s.part_rows = (long long)b.M * G < 128 ? b.M * G : 128;
+  return s;
+}
+
+template <int G>
+int launch(const Krea2PagedBatch& b, const PagedAttnArgs& pa, void* ws, cudaStream_t stream) {
+  static std::atomic<uint64_t> attr_done{0};
+  auto kern = paged_attn_tc_kernel<G>;
+  const uint64_t dev_bit = device_bit();
+  if (!(attr_done.load(std::memory_order_acquire) & dev_bit) || !dev_bit) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess ||
+        cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
+            cudaSuccess)
+      return set_error(KREA2_ERR_CUDA, "cudaFuncSetAttribute(paged attention) failed");
+    attr_done.fetch_or(dev_bit, std::memory_order_release);
+  }
+  const Shape sh = shape_of(b, pa.H, pa.Hkv);
+  Args a{};
+  a.b = PagedArgs{b.R, b.M, b.q_start, b.kv_len, b.page_table, b.max_pages, b.page_size, b.num_pages};
+  a.H = pa.H; a.Hkv = pa.Hkv; a.T = pa.T; a.eps = pa.eps; a.scale_log2 = pa.scale_log2;
+  a.qkvg = reinterpret_cast<const __nv_bfloat16*>(pa.qkvg);
+  a.qw = pa.q_norm_w; a.cos = pa.cos; a.sin = pa.sin; a.text_mask = pa.text_mask; a.key_end = pa.key_end;
+  a.out = reinterpret_cast<__nv_bfloat16*>(pa.out);
+  a.split = sh.split; a.ctas = sh.ctas; a.part_rows = sh.part_rows;
+  a.part_o = reinterpret_cast<float*>(ws);
+  a.part_ml = a.part_o + 2LL * sh.ctas * sh.part_rows * AD;
+  a.group = b.page_size % 64 == 0 ? 64 : b.page_size % 32 == 0 ? 32 : 16;
+  CUtensorMap tk, tv;
+  int rc;
+  if ((rc = make_tmap_pages(&tk, pa.k_pages, pa.Hkv, b, a.group)) || (rc = make_tmap_pages(&tv, pa.v_pages, pa.Hkv, b, a.group)))
+    return rc;
+  kern<<<sh.ctas, THREADS, SMEM_BYTES, stream>>>(tk, tv, a);
+  count_launch();
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess && sh.split && sh.ctas > 1) {
+    paged_attn_join_kernel<G><<<sh.ctas - 1, 256, 0, stream>>>(a);
+    count_launch();
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) return set_error(KREA2_ERR_CUDA, "paged attention launch failed: %s", cudaGetErrorString(e));
+  return KREA2_OK;
+}
+
+}  // namespace
+
+size_t paged_attn_tc_workspace(const Krea2PagedBatch& b, int H, int Hkv) {
+  const Shape s = shape_of(b, H, Hkv);
+  return s.split && s.ctas > 1 ? 2ull * s.ctas * s.part_rows * (AD + 2) * 4 : 0;
+}
+
+int launch_paged_attn_tc(const Krea2PagedBatch& b, const PagedAttnArgs& a, void* ws, cudaStream_t stream) {
+  switch (a.H / a.Hkv) {
+    case 1: return launch<1>(b, a, ws, stream);
+    case 2: return launch<2>(b, a, ws, stream);
+    default: return launch<4>(b, a, ws, stream);
+  }
+}
+
+}  // namespace krea2

@@ -552,7 +552,9 @@ __global__ void __launch_bounds__(gemm_threads<EPI>(), 1)
   gemm_body<BN, EPI, true, WIDE>(tmA, tmB, tmC, p, lt);
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
+}  // namespace
+
+PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   if (!fn) {
     void* ptr = nullptr;
@@ -564,13 +566,11 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
   return fn;
 }
 
-}  // namespace
-
 // Row-major bf16 matrix (rows, cols) as a 2-D TMA map with a (box_cols x box_rows) box and
 // 128-byte swizzle (box_cols * 2 bytes must be 128).
 int make_tmap_bf16_2d(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t row_stride_elems,
                       uint32_t box_cols, uint32_t box_rows) {
-  auto enc = get_encode_fn();
+  auto enc = tmap_encoder();
   if (!enc) return set_error(KREA2_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
   if ((reinterpret_cast<uintptr_t>(ptr) & 15) || ((row_stride_elems * 2) & 15))
     return set_error(KREA2_ERR_ARG, "TMA operand must be 16-byte aligned with a 16-byte multiple row stride");
@@ -590,7 +590,7 @@ int make_tmap_bf16_2d(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t r
 // Chunks and rows past the matrix read as zeros.
 int make_tmap_bf16_chunks(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t batches,
                           uint32_t box_rows, uint32_t box_chunks) {
-  auto enc = get_encode_fn();
+  auto enc = tmap_encoder();
   if (!enc) return set_error(KREA2_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
   if (reinterpret_cast<uintptr_t>(ptr) & 15) return set_error(KREA2_ERR_ARG, "TMA operand must be 16-byte aligned");
   cuuint64_t dims[4] = {64, rows, cols / 64, batches};
@@ -611,7 +611,7 @@ int make_tmap_bf16_chunks(CUtensorMap* m, const void* ptr, uint64_t cols, uint64
 // rows); rows at or beyond `rows` read as zeros, also when the buffer holds more.
 int make_tmap_bf16_3d(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t batches,
                       uint64_t row_stride_elems, uint32_t box_cols, uint32_t box_rows, uint64_t batch_rows) {
-  auto enc = get_encode_fn();
+  auto enc = tmap_encoder();
   if (!enc) return set_error(KREA2_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
   if ((reinterpret_cast<uintptr_t>(ptr) & 15) || ((row_stride_elems * 2) & 15))
     return set_error(KREA2_ERR_ARG, "TMA operand must be 16-byte aligned with a 16-byte multiple row stride");

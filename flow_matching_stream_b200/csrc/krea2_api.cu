@@ -295,10 +295,11 @@ const char* krea2_last_error_string(void) { return g_err; }
 int krea2_check_device_error(void* stream) {
   cudaError_t e = cudaStreamSynchronize(as_stream(stream));
   if (e != cudaSuccess) return set_error(KREA2_ERR_CUDA, "stream error: %s", cudaGetErrorString(e));
-  constexpr int FILES = 5;
+  constexpr int FILES = 6;
   const int ve[FILES] = {take_device_error_gemm(), take_device_error_attention(), take_device_error_paged(),
-                         take_device_error_lora(), take_device_error_lora_tc()};
-  const char* names[FILES] = {"GEMM", "attention", "paged cache", "adapter", "adapter"};
+                         take_device_error_lora(), take_device_error_lora_tc(),
+                         take_device_error_paged_tc()};
+  const char* names[FILES] = {"GEMM", "attention", "paged cache", "adapter", "adapter", "paged attention"};
   for (int i = 0; i < FILES; ++i) {
     if (ve[i] < 0) return set_error(KREA2_ERR_CUDA, "cannot read the device error word");
     if (ve[i] & ERR_WAIT_TIMEOUT)
@@ -868,7 +869,8 @@ int krea2_paged_kv_append(const Krea2Dims* dims, const Krea2PagedBatch* batch, i
 
 size_t krea2_paged_attention_workspace_size(const Krea2Dims* dims, const Krea2PagedBatch* batch, int dtype) {
   if (check_dims(dims, dtype) || check_batch_sizes(batch)) return 0;
-  return 0;
+  if (dtype != KREA2_BF16 || !attention_tc_supported(dims->D, dims->H, dims->Hkv)) return 0;
+  return paged_attn_tc_workspace(*batch, dims->H, dims->Hkv);
 }
 
 int krea2_gqa_attention_paged(const Krea2Dims* dims, const Krea2PagedBatch* batch, int T, int dtype, const void* qkvg,
@@ -890,6 +892,8 @@ int krea2_gqa_attention_paged(const Krea2Dims* dims, const Krea2PagedBatch* batc
   a.qkvg = qkvg; a.q_norm_w = q_norm_w; a.cos = cos; a.sin = sin;
   a.text_mask = T > 0 ? text_mask : nullptr; a.key_end = key_end;
   a.k_pages = batch->k_pages; a.v_pages = batch->v_pages; a.out = out;
+  if (dtype == KREA2_BF16 && attention_tc_supported(dims->D, dims->H, dims->Hkv))
+    return launch_paged_attn_tc(*batch, a, workspace, as_stream(stream));
   return launch_paged_attn_simt(*batch, a, dims->D, dtype == KREA2_BF16, as_stream(stream));
 }
 

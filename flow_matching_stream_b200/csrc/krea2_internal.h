@@ -1,6 +1,8 @@
 // Internal declarations shared by the library's translation units (not part of the ABI).
 #pragma once
 #include <atomic>
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -32,6 +34,10 @@ int take_device_error_attention();
 int take_device_error_paged();
 int take_device_error_lora();
 int take_device_error_lora_tc();
+int take_device_error_paged_tc();
+
+// cuTensorMapEncodeTiled of the driver, or null.
+PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder();
 
 struct GemmParams {
   int M, N, K;              // N = rows of W
@@ -172,6 +178,10 @@ struct PagedAttnArgs {
 int launch_paged_append(const Krea2PagedBatch& b, const Krea2Dims* d, bool bf16, const void* qkvg, const float* kw,
                         const float* cs, const float* sn, cudaStream_t stream);
 int launch_paged_attn_simt(const Krea2PagedBatch& b, const PagedAttnArgs& a, int D, bool bf16, cudaStream_t stream);
+
+// tensor-core path (bf16, attention_tc_supported): parts of cut items go through the workspace
+size_t paged_attn_tc_workspace(const Krea2PagedBatch& b, int H, int Hkv);
+int launch_paged_attn_tc(const Krea2PagedBatch& b, const PagedAttnArgs& a, void* ws, cudaStream_t stream);
 
 struct LoraLinearArgs {
   int M, N, K;

@@ -84,9 +84,11 @@ class Ragged:
         return k, v
 
     def attention(self, text_mask=None, key_end=None, k_pages=None, v_pages=None):
-        """(rows, H*D) in fp64; rows behind the last request are NaN."""
+        """(rows, H*D) in fp64, and sigmoid(g) sum_k p_k |v_k|, the size that errors of the probabilities are
+        relative to; rows behind the last request are NaN."""
         d = self.d
         out = torch.full((self.rows, d.HD), float("nan"), dtype=F64, device=self.qkvg.device)
+        size = out.clone()
         kp, vp = (self.k_pages if k_pages is None else k_pages), (self.v_pages if v_pages is None else v_pages)
         for r in range(self.R):
             n, L, sl = self.new[r], self.kv[r], self.rowsof(r)
@@ -115,8 +117,10 @@ class Ragged:
                 w = torch.exp(z - torch.where(top == -math.inf, 0.0, top))
                 total = w.sum(1, keepdim=True)
                 o = torch.where(total > 0, w @ v[:, j] / torch.where(total > 0, total, 1.0), 0.0)
+                a = torch.where(total > 0, w @ v[:, j].abs() / torch.where(total > 0, total, 1.0), 0.0)
                 out[sl, h * d.D:(h + 1) * d.D] = o * g[:, h]
-        return out
+                size[sl, h * d.D:(h + 1) * d.D] = a * g[:, h]
+        return out, size
 
 
 def lora_ref(A, W, down, up, scale, start, ids, epilogue, out0=None, gate=None, rows_per_batch=0):
