@@ -36,15 +36,24 @@ KREA2_DEFINE_ERROR_READER(take_device_error_paged_tc)
 namespace {
 
 constexpr int KT = 64;            // keys per tile
-constexpr int KV_STAGES = 2;
 constexpr int THREADS = 320;
 constexpr int SOFTMAX_THREADS = 256;
-constexpr int Q_CHUNK = 128 * 128;  // 128 rows x 64 bf16
 constexpr int KV_CHUNK = KT * 128;  // 64 keys x 64 bf16
 constexpr int KV_TILE_BYTES = 2 * KV_CHUNK;
-constexpr int OFF_K = 2 * Q_CHUNK;
-constexpr int OFF_V = OFF_K + KV_STAGES * KV_TILE_BYTES;
-constexpr int SMEM_BYTES = OFF_V + KV_STAGES * KV_TILE_BYTES + 1024;
+
+// FEW: batches of about one new token per request. Items have 16 MMA rows (16 / G tokens), which leaves the
+// room of the other queries to a third K/V stage: with few rows a tile's time is that of its loads. (The MMA
+// still reads 128 rows from each chunk of Q on, K's tiles behind the 16; those accumulator rows are not used.)
+template <int G, bool FEW>
+struct Cfg {
+  static constexpr int ROWS = FEW ? 16 : 128;   // query rows of an item
+  static constexpr int QPOS = ROWS / G;
+  static constexpr int STAGES = FEW ? 3 : 2;
+  static constexpr int Q_CHUNK = ROWS * 128;    // ROWS x 64 bf16
+  static constexpr int OFF_K = 2 * Q_CHUNK;
+  static constexpr int OFF_V = OFF_K + STAGES * KV_TILE_BYTES;
+  static constexpr int SMEM_BYTES = OFF_V + STAGES * KV_TILE_BYTES + 1024;
+};
 constexpr uint32_t TMEM_COLS = 256;  // S0 [0,64), S1 [64,128), O [128,256)
 constexpr uint32_t O_COL = 128;
 constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, KT, 0, 0);
@@ -65,10 +74,17 @@ struct Args {
   __nv_bfloat16* out;
   float* part_o;   // (2 CTAs, part_rows, 128)
   float* part_ml;  // (2 CTAs, part_rows, 2): maximum in powers of two, sum
+  struct Join* joins;  // (CTAs): the item that the start of each CTA's share cuts
   int part_rows;
   int group;       // keys per TMA box: 16, 32 or 64, a divisor of the page size
   int split;       // items may be cut
   int ctas;
+};
+
+// A cut item as paged_attn_join_kernel needs it: parts first.. last (CTA numbers), row0 the packed row of its
+// first token; rows 0: nothing to join at this place.
+struct Join {
+  int rows, row0, j, last;
 };
 
 struct ItemPlan {
@@ -77,17 +93,16 @@ struct ItemPlan {
   long long weight;                 // of the rest, in tiles (in items where items are not cut)
 };
 
-template <int G>
+template <int QPOS>
 __device__ __forceinline__ ItemPlan plan_of(const Args& a, int r, bool* bad) {
-  constexpr int QPOS = 128 / G;
   ItemPlan p;
   *bad = !request_rows(r, a.b.M, (long long)a.b.max_pages * a.b.page_size, a.b.q_start, a.b.kv_len, &p.q);
   if (*bad) p.q.n = 0;
   p.tiles = p.q.n ? (p.q.L + KT - 1) / KT : 1;
   p.qtiles = (p.q.n + QPOS - 1) / QPOS;
-  const long long items = (long long)p.qtiles * a.Hkv;
-  p.rounds = (int)(items / a.ctas);
-  p.rest = (int)(items % a.ctas);
+  const unsigned items = (unsigned)p.qtiles * (unsigned)a.Hkv;  // below 2^32: launch_paged_attn_tc checks it
+  p.rounds = (int)(items / (unsigned)a.ctas);
+  p.rest = (int)(items - (unsigned)p.rounds * (unsigned)a.ctas);
   p.weight = (long long)p.rest * (a.split ? p.tiles : 1);
   return p;
 }
@@ -99,7 +114,7 @@ struct Place {
   int r;                           // a.b.R: the place is behind the end
   int rounds;                      // whether a request has whole rounds
 };
-template <int G>
+template <int QPOS>
 __device__ Place find_place(const Args& a, int part, Place* shared, long long* warp_sums) {
   const int tid = threadIdx.x, nt = blockDim.x, warp = tid >> 5, lane = tid & 31;
   const int per = (a.b.R + nt - 1) / nt, r0 = min(tid * per, a.b.R), r1 = min(r0 + per, a.b.R);
@@ -107,7 +122,7 @@ __device__ Place find_place(const Args& a, int part, Place* shared, long long* w
   int rounds = 0;
   for (int r = r0; r < r1; ++r) {
     bool bad;
-    const ItemPlan p = plan_of<G>(a, r, &bad);
+    const ItemPlan p = plan_of<QPOS>(a, r, &bad);
     if (bad && blockIdx.x == 0) atomicOr(&g_device_error, ERR_BAD_BATCH);
     sum += p.weight;
     rounds |= p.rounds;
@@ -126,7 +141,9 @@ __device__ Place find_place(const Args& a, int part, Place* shared, long long* w
     if (w < warp) before += warp_sums[w];
     total += warp_sums[w];
   }
-  long long share = (total + a.ctas - 1) / a.ctas;
+  // 32-bit where it fits: a 64-bit division is a few hundred cycles of every CTA's start
+  const long long up = total + a.ctas - 1;
+  long long share = up <= 0xffffffffLL ? (long long)((unsigned)up / (unsigned)a.ctas) : up / a.ctas;
   if (a.split && share < MIN_SHARE) share = MIN_SHARE;
   if (share < 1) share = 1;
   const long long at = part * share, lo = before + incl - sum;
@@ -134,7 +151,7 @@ __device__ Place find_place(const Args& a, int part, Place* shared, long long* w
     long long left = at - lo;
     for (int r = r0; r < r1; ++r) {
       bool bad;
-      const ItemPlan p = plan_of<G>(a, r, &bad);
+      const ItemPlan p = plan_of<QPOS>(a, r, &bad);
       if (left < p.weight) {
         shared->r = r;
         shared->offset = left;
@@ -178,14 +195,15 @@ __device__ __forceinline__ uint32_t used_tiles(const Args& a, int r, int L, int 
   return __ballot_sync(0xffffffffu, used);
 }
 
-template <int G>
+template <int G, bool FEW>
 __global__ void __launch_bounds__(THREADS, 2)
     paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, Args a) {
-  constexpr int QPOS = 128 / G;
+  using C = Cfg<G, FEW>;
+  constexpr int QPOS = C::QPOS, STAGES = C::STAGES, Q_CHUNK = C::Q_CHUNK, OFF_K = C::OFF_K, OFF_V = C::OFF_V;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t seg_full[2], seg_empty[2];
   __shared__ __align__(8) uint64_t q_full;
-  __shared__ __align__(8) uint64_t k_full[KV_STAGES], k_empty[KV_STAGES], v_full[KV_STAGES], v_empty[KV_STAGES];
+  __shared__ __align__(8) uint64_t k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES];
   __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done[2];
   __shared__ __align__(8) uint64_t drain_bar;
   __shared__ uint32_t tmem_slot;
@@ -203,13 +221,15 @@ __global__ void __launch_bounds__(THREADS, 2)
     for (int s = 0; s < 2; ++s) {
       mbar_init(&seg_full[s], 1);
       mbar_init(&seg_empty[s], SOFTMAX_THREADS + 1);
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], SOFTMAX_THREADS);
+      mbar_init(&pv_done[s], 1);
+    }
+    for (int s = 0; s < STAGES; ++s) {
       mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 1);
       mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 1);
-      mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], SOFTMAX_THREADS);
-      mbar_init(&pv_done[s], 1);
     }
     mbar_init(&q_full, SOFTMAX_THREADS);
     mbar_init(&drain_bar, 1);
@@ -219,7 +239,9 @@ __global__ void __launch_bounds__(THREADS, 2)
     tma_prefetch_desc(&tmV);
   }
   if (warp == 1) tmem_alloc(&tmem_slot, TMEM_COLS);
-  const Place place = find_place<G>(a, blockIdx.x, &place_sh, warp_sums);
+  const Place place = find_place<QPOS>(a, blockIdx.x, &place_sh, warp_sums);
+  // the join kernel behind this grid may be made ready (it waits for this grid's end)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -229,6 +251,13 @@ __global__ void __launch_bounds__(THREADS, 2)
   if (warp == 0) {
     // ---- segments and K/V loads. The whole warp runs along; lane 0 signs for the bytes, lanes issue boxes.
     int it = 0, seg = 0;  // tiles and segments so far
+    int k_st = 0, k_ph = 0, v_st = 0, v_ph = 0;  // next stages of K and of V, and their phases
+    auto step = [](int& st, int& ph) {
+      if (++st == STAGES) {
+        st = 0;
+        ph ^= 1;
+      }
+    };
     IssuedFills k_fills, v_fills;
     const int per_page = a.b.page_size / a.group, boxes = KT / a.group;
     bool ok = true;
@@ -280,8 +309,8 @@ __global__ void __launch_bounds__(THREADS, 2)
       bool prev_has = false;
       int prev_count = 0;
       auto load_v = [&]() -> bool {
-        const int i = it - 1, st = i & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(&v_empty[st], ((i >> 1) & 1) ^ 1, abort))) return false;
+        const int st = v_st;
+        if (!__all_sync(0xffffffffu, mbar_wait(&v_empty[st], v_ph ^ 1, abort))) return false;
         uint8_t* vd = base + OFF_V + st * KV_TILE_BYTES;
         if (lane == 0) mbar_arrive_expect_tx(&v_full[st], prev_count * a.group * (2 * AD));
         __syncwarp();
@@ -291,7 +320,8 @@ __global__ void __launch_bounds__(THREADS, 2)
           tma_load_4d(vd + (lane & 1) * KV_CHUNK + (lane >> 1) * a.group * 128, &tmV, &v_full[st], 0, prev_slot,
                       s.j * 2 + (lane & 1), prev_page);
         }
-        v_fills.note(st, (i >> 1) & 1);
+        v_fills.note(st, v_ph);
+        step(v_st, v_ph);
         return true;
       };
       for (int t = t0; t < te; ++t) {
@@ -318,8 +348,8 @@ __global__ void __launch_bounds__(THREADS, 2)
         const int src = min(g0 - cached + (a.group == KT ? 0 : lane >> 1), 31);
         const int page = __shfl_sync(0xffffffffu, my_page, src), slot_in = __shfl_sync(0xffffffffu, my_slot, src);
         const bool has = (lane >> 1) < count;
-        const int st = it & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(&k_empty[st], ((it >> 1) & 1) ^ 1, abort))) return false;
+        const int st = k_st;
+        if (!__all_sync(0xffffffffu, mbar_wait(&k_empty[st], k_ph ^ 1, abort))) return false;
         uint8_t* kd = base + OFF_K + st * KV_TILE_BYTES;
         if (lane == 0) {
           tile_of[it % TILE_RING] = t;
@@ -332,7 +362,8 @@ __global__ void __launch_bounds__(THREADS, 2)
           tma_load_4d(kd + (lane & 1) * KV_CHUNK + (lane >> 1) * a.group * 128, &tmK, &k_full[st], 0, slot_in,
                       s.j * 2 + (lane & 1), page);
         }
-        k_fills.note(st, (it >> 1) & 1);
+        k_fills.note(st, k_ph);
+        step(k_st, k_ph);
         // V runs one tile behind K: V stages free up after P V only
         if (prev_tile >= 0 && !load_v()) return false;
         ++it;
@@ -348,13 +379,13 @@ __global__ void __launch_bounds__(THREADS, 2)
     if (place.rounds)
       for (int r = 0; r < a.b.R && ok; ++r) {
         bool bad;
-        const ItemPlan p = plan_of<G>(a, r, &bad);
+        const ItemPlan p = plan_of<QPOS>(a, r, &bad);
         for (int k = 0; k < p.rounds && ok; ++k) ok = run_item(p, r, k * a.ctas + blockIdx.x, 0, p.tiles, -1);
       }
     long long left = min(place.share, place.total - blockIdx.x * place.share), off = place.offset;
     for (int r = place.r; r < a.b.R && left > 0 && ok; ++r, off = 0) {
       bool bad;
-      const ItemPlan p = plan_of<G>(a, r, &bad);
+      const ItemPlan p = plan_of<QPOS>(a, r, &bad);
       const int unit = a.split ? p.tiles : 1;  // weight of an item
       while (off < p.weight && left > 0 && ok) {
         const int item = p.rounds * a.ctas + (int)(off / unit), from = (int)(off % unit);
@@ -372,8 +403,8 @@ __global__ void __launch_bounds__(THREADS, 2)
       publish(end);
     }
     if (*abort && lane == 0) {
-      k_fills.drain(k_full, KV_STAGES);
-      v_fills.drain(v_full, KV_STAGES);
+      k_fills.drain(k_full, STAGES);
+      v_fills.drain(v_full, STAGES);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -384,6 +415,13 @@ __global__ void __launch_bounds__(THREADS, 2)
       bool issued = false, ok = true;
       int it = 0;
       int queries = 0;  // segments with tiles so far
+      int k_st = 0, k_ph = 0, v_st = 0, v_ph = 0;
+      auto step = [](int& st, int& ph) {
+        if (++st == STAGES) {
+          st = 0;
+          ph ^= 1;
+        }
+      };
       for (int seg = 0; ok; ++seg) {
         if (!mbar_wait(&seg_full[seg & 1], (seg >> 1) & 1, abort)) break;
         const int n = segs[seg & 1].n, tiles = segs[seg & 1].tiles;
@@ -394,28 +432,29 @@ __global__ void __launch_bounds__(THREADS, 2)
         tc_fence_after();
         const int first = it;
         auto issue_pv = [&](int i) -> bool {
-          const int st = i & 1;
-          if (!mbar_wait2(&p_full[st], (i >> 1) & 1, &v_full[st], (i >> 1) & 1, abort)) return false;
+          const int sb = i & 1;
+          if (!mbar_wait2(&p_full[sb], (i >> 1) & 1, &v_full[v_st], v_ph, abort)) return false;
           tc_fence_after();
-          const uint64_t dv = dv0 + (uint64_t)(st * (KV_TILE_BYTES >> 4));
-          const uint32_t pt = tmem + st * KT;
+          const uint64_t dv = dv0 + (uint64_t)(v_st * (KV_TILE_BYTES >> 4));
+          const uint32_t pt = tmem + sb * KT;
 #pragma unroll
           for (int kk = 0; kk < KT / 16; ++kk)
             tc_mma_bf16_ts(tmem + O_COL, pt + kk * 8, dv + (uint64_t)(kk * 16 * 128 >> 4), IDESC_PV,
                            (i > first || kk > 0) ? 1u : 0u);
-          tc_commit(&pv_done[st]);
-          tc_commit(&v_empty[st]);
+          tc_commit(&pv_done[sb]);
+          tc_commit(&v_empty[v_st]);
+          step(v_st, v_ph);
           return true;
         };
         for (int i = 0; i < tiles; ++i, ++it) {
-          const int st = it & 1;
-          if (!mbar_wait(&k_full[st], (it >> 1) & 1, abort)) {
+          const int sb = it & 1;
+          if (!mbar_wait(&k_full[k_st], k_ph, abort)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t dk = dk0 + (uint64_t)(st * (KV_TILE_BYTES >> 4));
-          const uint32_t d_s = tmem + st * KT;
+          const uint64_t dk = dk0 + (uint64_t)(k_st * (KV_TILE_BYTES >> 4));
+          const uint32_t d_s = tmem + sb * KT;
 #pragma unroll
           for (int kk = 0; kk < AD / 16; ++kk) {
             const uint32_t qo = (kk >> 2) * Q_CHUNK + (kk & 3) * 32;
@@ -423,8 +462,9 @@ __global__ void __launch_bounds__(THREADS, 2)
             tc_mma_bf16(d_s, dq0 + (uint64_t)(qo >> 4), dk + (uint64_t)(ko >> 4), IDESC_QK, kk > 0 ? 1u : 0u);
           }
           issued = true;
-          tc_commit(&s_full[st]);
-          tc_commit(&k_empty[st]);
+          tc_commit(&s_full[sb]);
+          tc_commit(&k_empty[k_st]);
+          step(k_st, k_ph);
           if (i >= 1 && !issue_pv(it - 1)) {
             ok = false;
             break;
@@ -448,7 +488,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     const float sl2 = a.scale_log2;
     const long long qc = 2LL * (a.H + a.Hkv) * AD;
     constexpr int HK = KT / 2;
-    int it = 0, seg = 0;
+    int it = 0, seg = 0, v_st = 0, v_ph = 0;
     Segment s;
     // Segment's queries, normalised and rotated, into shared memory (row = token * G + head, 128-byte swizzle)
     auto next_segment = [&]() -> bool {
@@ -502,7 +542,11 @@ __global__ void __launch_bounds__(THREADS, 2)
       if (a.key_end && tok < cur.n) row_kend = min(max(a.key_end[cur.row0 + tok], cur.pos0 + tok + 1), cur.L);
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < cur.tiles; ++i, ++it) {
-        const int sb = it & 1;
+        const int sb = it & 1, st = v_st, ph = v_ph;
+        if (++v_st == STAGES) {
+          v_st = 0;
+          v_ph ^= 1;
+        }
         if (!__all_sync(0xffffffffu, mbar_wait(&s_full[sb], (it >> 1) & 1, abort))) {
           ok = false;
           break;
@@ -515,14 +559,14 @@ __global__ void __launch_bounds__(THREADS, 2)
           vm0 = __ballot_sync(0xffffffffu, key_used(a, cur.r, cur.L, t0 + lane));
           vm1 = __ballot_sync(0xffffffffu, key_used(a, cur.r, cur.L, t0 + 32 + lane));
           if ((vm0 & vm1) != 0xffffffffu) {  // the same for all warps: clear the V rows of unused keys
-            if (!__all_sync(0xffffffffu, mbar_wait(&v_full[sb], (it >> 1) & 1, abort))) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&v_full[st], ph, abort))) {
               ok = false;
               break;
             }
             const int key = (threadIdx.x - 64) >> 2, part = threadIdx.x & 3;
             const uint32_t vm = key < 32 ? vm0 : vm1;
             if (!((vm >> (key & 31)) & 1u)) {
-              uint8_t* v = base + OFF_V + sb * KV_TILE_BYTES + (part >> 1) * KV_CHUNK + key * 128 + (part & 1) * 64;
+              uint8_t* v = base + OFF_V + st * KV_TILE_BYTES + (part >> 1) * KV_CHUNK + key * 128 + (part & 1) * 64;
 #pragma unroll
               for (int q = 0; q < 4; ++q) reinterpret_cast<uint4*>(v)[q] = make_uint4(0u, 0u, 0u, 0u);
             }
@@ -645,6 +689,24 @@ __global__ void __launch_bounds__(THREADS, 2)
     }
   }
 
+  if (a.joins && threadIdx.x == 32) {  // what it joins at the start of this CTA's share
+    Join x{};
+    if (place.r < a.b.R) {
+      bool bad;
+      const ItemPlan p = plan_of<QPOS>(a, place.r, &bad);
+      const int nth = (int)(place.offset / p.tiles), within = (int)(place.offset - (long long)nth * p.tiles);
+      // only the first place that cuts an item joins it
+      const long long start = (long long)blockIdx.x * place.share - within;
+      if (within > 0 && start >= ((long long)blockIdx.x - 1) * place.share) {
+        const int item = p.rounds * a.ctas + nth, qt = item % p.qtiles;
+        x.j = item / p.qtiles;
+        x.rows = min(QPOS, p.q.n - qt * QPOS) * G;
+        x.row0 = p.q.row0 + qt * QPOS;
+        x.last = (int)((start + p.tiles - 1) / place.share);
+      }
+    }
+    a.joins[blockIdx.x] = x;
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -653,48 +715,39 @@ __global__ void __launch_bounds__(THREADS, 2)
   }
 }
 
-// Joins the parts of cut items: block c looks at the place where CTA c's share starts, and joins the item
-// that is cut there if no earlier place cuts it. Parts come in key order, so results repeat bit for bit.
+constexpr int JOIN_ROWS = 16;
+
+// Joins the parts of cut items: block (c, y), for 16 rows, looks at the place where CTA c's share starts, and
+// joins the item that is cut there if no earlier place cuts it. Parts come in key order, so results repeat bit
+// for bit. Launched as a programmatic dependent of the kernel above.
 template <int G>
 __global__ void __launch_bounds__(256) paged_attn_join_kernel(Args a) {
-  constexpr int QPOS = 128 / G;
-  __shared__ Place place_sh;
-  __shared__ long long warp_sums[8];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Place place = find_place<G>(a, c, &place_sh, warp_sums);
-  if (place.r >= a.b.R) return;
-  bool bad;
-  const ItemPlan p = plan_of<G>(a, place.r, &bad);
-  const int within = (int)(place.offset % p.tiles);
-  if (within == 0) return;  // the share starts with an item
-  const long long start = (long long)c * place.share - within;
-  if (start / place.share + 1 != c) return;
-  const int last = (int)((start + p.tiles - 1) / place.share);
-  const int item = p.rounds * a.ctas + (int)(place.offset / p.tiles);
-  const int qt = item % p.qtiles, j = item / p.qtiles;
-  const int rows = min(QPOS, p.q.n - qt * QPOS) * G;
+  const Join x = a.joins[c];
   const long long qc = 2LL * (a.H + a.Hkv) * AD;
-  for (int row = warp; row < rows; row += 8) {
+  const int end = min(x.rows, (int)(blockIdx.y + 1) * JOIN_ROWS);
+  for (int row = blockIdx.y * JOIN_ROWS + warp; row < end; row += 8) {
+    const int h = x.j * G + row % G;
+    const long long prow = x.row0 + row / G;
+    const uint2 g = *reinterpret_cast<const uint2*>(a.qkvg + prow * qc + (a.H + 2 * a.Hkv + h) * AD + lane * 4);
     const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + row;
     auto slot_of = [&](int k) { return (long long)(k < c ? 2 * (c - 1) + 1 : 2 * k) * a.part_rows; };
-    float top = -INFINITY;
-    for (int k = c - 1; k <= last; ++k) top = fmaxf(top, ml[slot_of(k)].x);
-    float o[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
-    for (int k = c - 1; k <= last; ++k) {
+    float o[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f, top = -INFINITY;
+    for (int k = c - 1; k <= x.last; ++k) {
       const float2 v = ml[slot_of(k)];
+      const float4 y = *reinterpret_cast<const float4*>(a.part_o + (slot_of(k) + row) * AD + lane * 4);
       if (v.x == -INFINITY && v.y == 0.f) continue;  // no readable key in this part
-      const float w = ex2(v.x - top);
-      const float4 x = *reinterpret_cast<const float4*>(a.part_o + (slot_of(k) + row) * AD + lane * 4);
-      sum += w * v.y;
-      o[0] += w * x.x;
-      o[1] += w * x.y;
-      o[2] += w * x.z;
-      o[3] += w * x.w;
+      const float m = fmaxf(top, v.x);
+      const float old = top == -INFINITY ? 0.f : ex2(top - m), w = ex2(v.x - m);
+      sum = sum * old + w * v.y;
+      o[0] = o[0] * old + w * y.x;
+      o[1] = o[1] * old + w * y.y;
+      o[2] = o[2] * old + w * y.z;
+      o[3] = o[3] * old + w * y.w;
+      top = m;
     }
     const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-    const int h = j * G + row % G;
-    const long long prow = p.q.row0 + qt * QPOS + row / G;
-    const uint2 g = *reinterpret_cast<const uint2*>(a.qkvg + prow * qc + (a.H + 2 * a.Hkv + h) * AD + lane * 4);
     uint2 r;
     r.x = pack_bf16x2(o[0] * inv * sigmoid_f(bf16_lo(g.x)), o[1] * inv * sigmoid_f(bf16_hi(g.x)));
     r.y = pack_bf16x2(o[2] * inv * sigmoid_f(bf16_lo(g.y)), o[3] * inv * sigmoid_f(bf16_hi(g.y)));
@@ -720,24 +773,33 @@ int make_tmap_pages(CUtensorMap* m, const void* ptr, int Hkv, const Krea2PagedBa
 
 // Launch sizes from what the host knows: row and request counts and the longest sequence the table holds.
 struct Shape {
-  int ctas, split, part_rows;
+  int few, ctas, split, part_rows;
+  size_t o_bytes, ml_bytes, join_bytes;
 };
 Shape shape_of(const Krea2PagedBatch& b, int H, int Hkv) {
-  const int G = H / Hkv, qpos = 128 / G;
+  const int G = H / Hkv;
+  Shape s;
+  // about one new token per request, or so few that an item of 16 rows holds them
+  s.few = b.M <= 2LL * b.R || b.M * (long long)G <= 16;
+  const int rows = s.few ? 16 : 128, qpos = rows / G;
   const long long qtiles = b.M < b.M / qpos + b.R ? b.M : b.M / qpos + (long long)b.R;
   const long long tiles = ((long long)b.max_pages * b.page_size + KT - 1) / KT;
-  Shape s;
   s.split = tiles > MIN_SHARE;
   const long long most = qtiles * Hkv * (s.split ? (tiles + MIN_SHARE - 1) / MIN_SHARE : 1);
   s.ctas = (int)(most < 2LL * num_sms() ? most : 2LL * num_sms());
-  s.part_rows = (long long)b.M * G < 128 ? b.M * G : 128;
+  if (s.ctas == 1) s.split = 0;
+  s.part_rows = (long long)b.M * G < rows ? b.M * G : rows;
+  s.o_bytes = s.split ? 2ull * s.ctas * s.part_rows * AD * 4 : 0;
+  s.ml_bytes = s.split ? 2ull * s.ctas * s.part_rows * 2 * 4 : 0;
+  s.join_bytes = s.split ? sizeof(Join) * s.ctas : 0;
   return s;
 }
 
-template <int G>
-int launch(const Krea2PagedBatch& b, const PagedAttnArgs& pa, void* ws, cudaStream_t stream) {
+template <int G, bool FEW>
+int launch(const Krea2PagedBatch& b, const PagedAttnArgs& pa, const Shape& sh, void* ws, cudaStream_t stream) {
+  constexpr int SMEM_BYTES = Cfg<G, FEW>::SMEM_BYTES;
   static std::atomic<uint64_t> attr_done{0};
-  auto kern = paged_attn_tc_kernel<G>;
+  auto kern = paged_attn_tc_kernel<G, FEW>;
   const uint64_t dev_bit = device_bit();
   if (!(attr_done.load(std::memory_order_acquire) & dev_bit) || !dev_bit) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess ||
@@ -746,7 +808,6 @@ int launch(const Krea2PagedBatch& b, const PagedAttnArgs& pa, void* ws, cudaStre
       return set_error(KREA2_ERR_CUDA, "cudaFuncSetAttribute(paged attention) failed");
     attr_done.fetch_or(dev_bit, std::memory_order_release);
   }
-  const Shape sh = shape_of(b, pa.H, pa.Hkv);
   Args a{};
   a.b = PagedArgs{b.R, b.M, b.q_start, b.kv_len, b.page_table, b.max_pages, b.page_size, b.num_pages};
   a.H = pa.H; a.Hkv = pa.Hkv; a.T = pa.T; a.eps = pa.eps; a.scale_log2 = pa.scale_log2;
@@ -754,8 +815,12 @@ int launch(const Krea2PagedBatch& b, const PagedAttnArgs& pa, void* ws, cudaStre
   a.qw = pa.q_norm_w; a.cos = pa.cos; a.sin = pa.sin; a.text_mask = pa.text_mask; a.key_end = pa.key_end;
   a.out = reinterpret_cast<__nv_bfloat16*>(pa.out);
   a.split = sh.split; a.ctas = sh.ctas; a.part_rows = sh.part_rows;
-  a.part_o = reinterpret_cast<float*>(ws);
-  a.part_ml = a.part_o + 2LL * sh.ctas * sh.part_rows * AD;
+  if (sh.split) {
+    uint8_t* w = reinterpret_cast<uint8_t*>(ws);
+    a.part_o = reinterpret_cast<float*>(w);
+    a.part_ml = reinterpret_cast<float*>(w + sh.o_bytes);
+    a.joins = reinterpret_cast<Join*>(w + sh.o_bytes + sh.ml_bytes);
+  }
   a.group = b.page_size % 64 == 0 ? 64 : b.page_size % 32 == 0 ? 32 : 16;
   CUtensorMap tk, tv;
   int rc;
@@ -764,27 +829,43 @@ int launch(const Krea2PagedBatch& b, const PagedAttnArgs& pa, void* ws, cudaStre
   kern<<<sh.ctas, THREADS, SMEM_BYTES, stream>>>(tk, tv, a);
   count_launch();
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && sh.split && sh.ctas > 1) {
-    paged_attn_join_kernel<G><<<sh.ctas - 1, 256, 0, stream>>>(a);
+  if (e == cudaSuccess && sh.split) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(sh.ctas - 1, (sh.part_rows + JOIN_ROWS - 1) / JOIN_ROWS);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<G>, a);
     count_launch();
-    e = cudaGetLastError();
   }
   if (e != cudaSuccess) return set_error(KREA2_ERR_CUDA, "paged attention launch failed: %s", cudaGetErrorString(e));
   return KREA2_OK;
+}
+
+template <int G>
+int launch_g(const Krea2PagedBatch& b, const PagedAttnArgs& a, void* ws, cudaStream_t stream) {
+  const Shape s = shape_of(b, a.H, a.Hkv);
+  return s.few ? launch<G, true>(b, a, s, ws, stream) : launch<G, false>(b, a, s, ws, stream);
 }
 
 }  // namespace
 
 size_t paged_attn_tc_workspace(const Krea2PagedBatch& b, int H, int Hkv) {
   const Shape s = shape_of(b, H, Hkv);
-  return s.split && s.ctas > 1 ? 2ull * s.ctas * s.part_rows * (AD + 2) * 4 : 0;
+  return s.o_bytes + s.ml_bytes + s.join_bytes;
 }
 
 int launch_paged_attn_tc(const Krea2PagedBatch& b, const PagedAttnArgs& a, void* ws, cudaStream_t stream) {
+  if ((long long)b.M * a.Hkv > 0x7fffffffLL)  // items (at most one per token and KV head) are counted in 32 bits
+    return set_error(KREA2_ERR_UNSUPPORTED, "too many rows x KV heads (%lld)", (long long)b.M * a.Hkv);
   switch (a.H / a.Hkv) {
-    case 1: return launch<1>(b, a, ws, stream);
-    case 2: return launch<2>(b, a, ws, stream);
-    default: return launch<4>(b, a, ws, stream);
+    case 1: return launch_g<1>(b, a, ws, stream);
+    case 2: return launch_g<2>(b, a, ws, stream);
+    default: return launch_g<4>(b, a, ws, stream);
   }
 }
 

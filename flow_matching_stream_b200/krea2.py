@@ -325,17 +325,51 @@ def backbone_forward(dims, B: int, T: int, N: int, hidden_states: torch.Tensor, 
 
 # ----------------------------------------------------------------------------- ragged batches
 
-def _on(device: torch.device, stream, *tensors: Optional[torch.Tensor]) -> int:
-    """The stream to launch on, once every tensor and the stream are known to be on the current device."""
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"expected all tensors on {device}, got one on {t.device}")
+# These calls are short next to what a checked argument costs in Python, so each tensor is checked by one
+# function that looks at nothing twice and words its complaint only when there is one.
+
+def _complain(t: Optional[torch.Tensor], dev: int, dtype: torch.dtype, shape: tuple, name: str) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    raise ValueError(f"{name}: expected a contiguous tensor")
+
+
+def _arg(t: torch.Tensor, dev: int, dtype: torch.dtype, shape: tuple, name: str) -> int:
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _complain(t, dev, dtype, shape, name)
+
+
+def _ws(t: Optional[torch.Tensor], dev: int) -> tuple:
+    if t is None:
+        return None, 0
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on cuda:{dev}")
+    return t.data_ptr(), t.nbytes
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on(dev: int, stream) -> int:
+    """The stream to launch on, once it and the tensors are known to belong to the current device."""
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
     if stream is None:
-        stream = torch.cuda.current_stream()
-    elif stream.device != device:
-        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
+        return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+    if stream.device.index != dev:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to cuda:{dev}")
     return stream.cuda_stream
 
 
@@ -370,8 +404,9 @@ class PagedBatch:
         s.q_start, s.kv_len, s.page_table, s.k_pages, s.v_pages = (_p(t) for t in self.tensors)
         if any(t.device != self.device for t in self.tensors):
             raise ValueError("the batch's tensors must be on one device")
-        self.rows, self.kv_cols = rows, k_pages.shape[2]
+        self.dev, self.R, self.rows, self.kv_cols = k_pages.get_device(), R, rows, k_pages.shape[2]
         self.struct = s
+        self.ref = ctypes.byref(s)
 
 
 def paged_batch_check(q_start, kv_len, page_table, num_pages: int, page_size: int, rows: int) -> None:
@@ -386,28 +421,25 @@ def paged_batch_check(q_start, kv_len, page_table, num_pages: int, page_size: in
     _check(lib().krea2_paged_batch_check(ctypes.byref(s)))
 
 
-def _paged_args(d: _lib.Krea2Dims, batch: PagedBatch, qkvg: torch.Tensor, norm_w: torch.Tensor, cos: torch.Tensor,
-                sin: torch.Tensor) -> None:
-    if batch.dtype != qkvg.dtype:
-        raise TypeError(f"the pages are {batch.dtype}, qkvg is {qkvg.dtype}")
+def _paged_cols(d: _lib.Krea2Dims, batch: PagedBatch) -> None:
     if batch.kv_cols != d.Hkv * d.D:
         raise ValueError(f"the pages have {batch.kv_cols} columns, the model has Hkv*D = {d.Hkv * d.D}")
-    _shape(qkvg, (batch.rows, 2 * (d.H + d.Hkv) * d.D), "qkvg")
-    for t, n in ((norm_w, "norm weight"), (cos, "cos"), (sin, "sin")):
-        _want(t, torch.float32, n)
-    _shape(norm_w, (d.D,), "norm weight")
-    _shape(cos, (batch.rows, d.D // 2), "cos")
-    _shape(sin, (batch.rows, d.D // 2), "sin")
 
 
 def paged_kv_append(dims, batch: PagedBatch, qkvg: torch.Tensor, k_norm_w: torch.Tensor, cos: torch.Tensor,
                     sin: torch.Tensor, stream=None) -> None:
     """Keys and values of a ragged batch's new tokens into its pages."""
-    d = dims_struct(dims)
-    _paged_args(d, batch, qkvg, k_norm_w, cos, sin)
-    st = _on(batch.device, stream, qkvg, k_norm_w, cos, sin)
-    _check(lib().krea2_paged_kv_append(ctypes.byref(d), ctypes.byref(batch.struct), dtype_code(qkvg.dtype), _p(qkvg),
-                                       _p(k_norm_w), _p(cos), _p(sin), st))
+    d = dims if isinstance(dims, _lib.Krea2Dims) else dims_struct(dims)
+    dev, rows, D = batch.dev, batch.rows, d.D
+    _paged_cols(d, batch)
+    table = (rows, D // 2)
+    rc = lib().krea2_paged_kv_append(
+        ctypes.byref(d), batch.ref, dtype_code(batch.dtype),
+        _arg(qkvg, dev, batch.dtype, (rows, 2 * (d.H + d.Hkv) * D), "qkvg"),
+        _arg(k_norm_w, dev, torch.float32, (D,), "k_norm_w"), _arg(cos, dev, torch.float32, table, "cos"),
+        _arg(sin, dev, torch.float32, table, "sin"), _stream_on(dev, stream))
+    if rc:
+        _check(rc)
 
 
 def paged_attention_workspace_size(dims, batch: PagedBatch, dtype: torch.dtype) -> int:
@@ -419,23 +451,25 @@ def gqa_attention_paged(dims, batch: PagedBatch, qkvg: torch.Tensor, q_norm_w: t
                         sin: torch.Tensor, text_mask: Optional[torch.Tensor], key_end: Optional[torch.Tensor],
                         out: torch.Tensor, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """Attention of a ragged batch's new tokens over its pages; text_mask (R, T) uint8, key_end (rows) int32."""
-    d = dims_struct(dims)
-    _paged_args(d, batch, qkvg, q_norm_w, cos, sin)
-    _want(out, qkvg.dtype, "out")
-    _shape(out, (batch.rows, d.H * d.D), "out")
-    T = 0
+    d = dims if isinstance(dims, _lib.Krea2Dims) else dims_struct(dims)
+    dev, rows, D = batch.dev, batch.rows, d.D
+    _paged_cols(d, batch)
+    table = (rows, D // 2)
+    T, mask, end = 0, None, None
     if text_mask is not None:
-        _want(text_mask, torch.uint8, "text_mask")
         T = text_mask.shape[-1]
-        _shape(text_mask, (batch.struct.R, T), "text_mask")
+        mask = _arg(text_mask, dev, torch.uint8, (batch.R, T), "text_mask")
     if key_end is not None:
-        _want(key_end, torch.int32, "key_end")
-        _shape(key_end, (batch.rows,), "key_end")
-    st = _on(batch.device, stream, qkvg, q_norm_w, cos, sin, text_mask, key_end, out, workspace)
-    ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().krea2_gqa_attention_paged(ctypes.byref(d), ctypes.byref(batch.struct), T, dtype_code(qkvg.dtype),
-                                           _p(qkvg), _p(q_norm_w), _p(cos), _p(sin), _p(text_mask), _p(key_end),
-                                           _p(out), _p(workspace), ws, st))
+        end = _arg(key_end, dev, torch.int32, (rows,), "key_end")
+    ws, ws_bytes = _ws(workspace, dev)
+    rc = lib().krea2_gqa_attention_paged(
+        ctypes.byref(d), batch.ref, T, dtype_code(batch.dtype),
+        _arg(qkvg, dev, batch.dtype, (rows, 2 * (d.H + d.Hkv) * D), "qkvg"),
+        _arg(q_norm_w, dev, torch.float32, (D,), "q_norm_w"), _arg(cos, dev, torch.float32, table, "cos"),
+        _arg(sin, dev, torch.float32, table, "sin"), mask, end,
+        _arg(out, dev, batch.dtype, (rows, d.H * D), "out"), ws, ws_bytes, _stream_on(dev, stream))
+    if rc:
+        _check(rc)
 
 
 class LoraAdapters:
@@ -457,6 +491,7 @@ class LoraAdapters:
         self.struct = _lib.Krea2Lora()
         self.struct.n_adapters, self.struct.rank = n, self.rank
         self.struct.down, self.struct.up, self.struct.scale = _p(down), _p(up), _p(scale)
+        self.dev = down.get_device()
 
     @staticmethod
     def fused(parts: Sequence[Sequence[tuple]], scale: torch.Tensor) -> "LoraAdapters":
@@ -489,37 +524,31 @@ def lora_linear(epilogue: int, A: torch.Tensor, W: torch.Tensor, adapters: LoraA
 
     rows_per_batch = 0 gates a residual with the gate row of the row's request; gate_stride None is the
     gate's row length."""
-    M, K = A.shape
-    Nw = W.shape[0]
-    if W.shape[1] != K:
-        raise ValueError("A and W disagree on K")
-    _want(W, A.dtype, "W")
-    _want(adapters.down, A.dtype, "adapters")
-    if adapters.K != K or adapters.Nw != Nw:
-        raise ValueError(f"adapters are for a ({adapters.Nw}, {adapters.K}) projection, W is ({Nw}, {K})")
-    _want(row_start, torch.int32, "row_start")
-    _want(adapter, torch.int32, "adapter")
-    R = adapter.shape[0]
-    _shape(row_start, (R + 1,), "row_start")
-    _shape(adapter, (R,), "adapter")
+    dev, dt, K, Nw, R = adapters.dev, adapters.dtype, adapters.K, adapters.Nw, adapter.shape[0]
+    M = A.shape[0]
     resid = epilogue == KREA2_EPI_RESID
-    _want(out, torch.float32 if resid else A.dtype, "out")
-    _shape(out, (M, Nw // 2 if epilogue == KREA2_EPI_SWIGLU else Nw), "out")
+    gate_p = None
     if resid:
         if gate is None:
             raise ValueError("a residual epilogue needs a gate")
-        _want(gate, torch.float32, "gate")
         if gate_stride is None:
             gate_stride = gate.shape[-1]
         rows = R if rows_per_batch == 0 else (M + rows_per_batch - 1) // max(rows_per_batch, 1)
         if gate.numel() < (rows - 1) * gate_stride + Nw:
             raise ValueError(f"the gate has {gate.numel()} values, {rows} rows of stride {gate_stride} are read")
-    st = _on(A.device, stream, W, adapters.down, row_start, adapter, out, workspace, gate)
+        gate_p = _arg(gate, dev, torch.float32, gate.shape, "gate")
+    ws, ws_bytes = _ws(workspace, dev)
     s = _lib.Krea2Lora.from_buffer_copy(adapters.struct)
-    s.R, s.row_start, s.adapter = R, _p(row_start), _p(adapter)
-    _check(lib().krea2_lora_linear(dtype_code(A.dtype), epilogue, M, Nw, K, _p(A), _p(W), ctypes.byref(s), _p(out),
-                                   _p(gate), rows_per_batch, gate_stride or 0, _p(workspace),
-                                   workspace.numel() * workspace.element_size(), st))
+    s.R = R
+    s.row_start = _arg(row_start, dev, torch.int32, (R + 1,), "row_start")
+    s.adapter = _arg(adapter, dev, torch.int32, (R,), "adapter")
+    rc = lib().krea2_lora_linear(
+        dtype_code(dt), epilogue, M, Nw, K, _arg(A, dev, dt, (M, K), "A"), _arg(W, dev, dt, (Nw, K), "W"),
+        ctypes.byref(s),
+        _arg(out, dev, torch.float32 if resid else dt, (M, Nw // 2 if epilogue == KREA2_EPI_SWIGLU else Nw), "out"),
+        gate_p, rows_per_batch, gate_stride or 0, ws, ws_bytes, _stream_on(dev, stream))
+    if rc:
+        _check(rc)
 
 
 # ----------------------------------------------------------------------------- weights
