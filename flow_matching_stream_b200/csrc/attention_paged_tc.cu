@@ -183,16 +183,23 @@ __device__ __forceinline__ bool key_used(const Args& a, int r, int L, int t) {
   return !(a.text_mask && t < a.T) || a.text_mask[(long long)r * a.T + t] != 0;
 }
 
-// Whether each of 32 tiles from t0 on (one per lane) has a key to compute.
+// Whether each of the 32 tiles from t0 on (below t1, and wholly among the request's first T keys) has a key to
+// compute: bit i for tile t0 + i. The whole warp reads a tile's 64 mask bytes at once, four tiles in flight.
 __device__ __forceinline__ uint32_t used_tiles(const Args& a, int r, int L, int t0, int t1, int lane) {
-  const int t = t0 + lane;
-  bool used = false;
-  if (t < t1) {
-    const int k0 = t * KT, k1 = min(k0 + KT, L);
-    used = !a.text_mask || k1 > a.T;
-    for (int k = k0; k < k1 && !used; ++k) used = a.text_mask[(long long)r * a.T + k] != 0;
+  const uint8_t* mask = a.text_mask + (long long)r * a.T;
+  uint32_t word = 0;
+  for (int i = 0; i < 32 && t0 + i < t1; i += 4) {
+    bool used[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int k = (t0 + i + q) * KT + lane, end = t0 + i + q < t1 ? L : 0;
+      const uint8_t m0 = k < end ? mask[k] : 0, m1 = k + 32 < end ? mask[k + 32] : 0;
+      used[q] = (m0 | m1) != 0;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) word |= (uint32_t)__any_sync(0xffffffffu, used[q]) << (i + q);
   }
-  return __ballot_sync(0xffffffffu, used);
+  return word;
 }
 
 template <int G, bool FEW>
@@ -260,6 +267,10 @@ __global__ void __launch_bounds__(THREADS, 2)
     };
     IssuedFills k_fills, v_fills;
     const int per_page = a.b.page_size / a.group, boxes = KT / a.group;
+    // Of the last request looked at: the tiles with keys to compute from mask_t0 on, and lane i's page and slot of box
+    // `cached` + i. The items of a request's heads and tokens follow one another and start with the same tiles.
+    int mask_r = -1, mask_t0 = 0, page_r = -1, cached = 0, my_page = 0, my_slot = 0;
+    uint32_t mask_word = 0;
     bool ok = true;
 
     auto publish = [&](const Segment& s) -> bool {
@@ -296,14 +307,28 @@ __global__ void __launch_bounds__(THREADS, 2)
       }
       s.tiles = max(te - t0, 0);
       const int text_tiles = a.text_mask ? min(te, a.T / KT) : 0;  // tiles that may hold masked keys only
-      for (int t = t0; t < text_tiles; t += 32)
-        s.tiles -= min(32, text_tiles - t) - __popc(used_tiles(a, r, p.q.L, t, text_tiles, lane));
+      const int all_text = a.text_mask ? min(p.tiles, a.T / KT) : 0;
+      uint32_t first_used = 0;
+      for (int t = t0; t < text_tiles; t += 32) {
+        uint32_t w;
+        if (t == t0) {
+          if (mask_r != r || mask_t0 != t0) {
+            mask_word = used_tiles(a, r, p.q.L, t0, all_text, lane);
+            mask_r = r;
+            mask_t0 = t0;
+          }
+          w = first_used = mask_word;
+        } else {
+          w = used_tiles(a, r, p.q.L, t, all_text, lane);
+        }
+        if (text_tiles - t < 32) w &= (1u << (text_tiles - t)) - 1u;
+        s.tiles -= min(32, text_tiles - t) - __popc(w);
+      }
       if (!publish(s)) return false;
 
       const int32_t* pages = a.b.page_table + (long long)r * a.b.max_pages;
       const int groups = (p.q.L + a.group - 1) / a.group;  // boxes that hold keys
       uint32_t used = 0;
-      int my_page = 0, my_slot = 0, cached = -1;  // lane i: page and slot of box cached + i
       int prev_tile = -1;                          // the tile whose V is still to be loaded
       int prev_page = 0, prev_slot = 0;
       bool prev_has = false;
@@ -326,12 +351,14 @@ __global__ void __launch_bounds__(THREADS, 2)
       };
       for (int t = t0; t < te; ++t) {
         if (t < text_tiles) {
-          if (t == t0 || (t - t0) % 32 == 0) used = used_tiles(a, r, p.q.L, t, text_tiles, lane);
+          if (t == t0) used = first_used;
+          else if ((t - t0) % 32 == 0) used = used_tiles(a, r, p.q.L, t, all_text, lane);
           if (!((used >> ((t - t0) & 31)) & 1u)) continue;
         }
         // pages of the tile's boxes: 32 boxes looked up at once
         const int g0 = t * boxes;
-        if (cached < 0 || g0 + boxes > cached + 32) {
+        if (page_r != r || g0 < cached || g0 + boxes > cached + 32) {
+          page_r = r;
           cached = g0;
           const int g = g0 + lane;
           my_page = a.b.num_pages;  // outside the pool: reads as zeros
@@ -636,6 +663,17 @@ __global__ void __launch_bounds__(THREADS, 2)
       // starts while this segment's output is written
       ++seg;
       const bool more = next_segment();
+      // the gates of a whole item, on their way before the last product is waited for
+      const bool row_ok = tok < cur.n;
+      const int h = cur.j * G + row % G;
+      const long long prow = cur.row0 + tok;
+      const uint4* gp =
+          reinterpret_cast<const uint4*>(a.qkvg + prow * qc + (a.H + 2 * a.Hkv + h) * AD + half * (AD / 2));
+      uint4 gates[4];
+      const bool gated = active && row_ok && cur.slot < 0;
+      if (gated)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) gates[q] = __ldg(gp + q);
       if (cur.tiles > 0) {
         const int i = it - 1;
         if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[i & 1], (i >> 1) & 1, abort))) break;
@@ -643,10 +681,7 @@ __global__ void __launch_bounds__(THREADS, 2)
       }
       if (active) {
         const float lt = l + __shfl_xor_sync(0xffffffffu, l, 16);
-        const bool row_ok = tok < cur.n;
         const float inv_l = lt > 0.f ? 1.f / lt : (lt == 0.f ? 0.f : lt);  // no readable key: zeros; NaN stays
-        const int h = cur.j * G + row % G;
-        const long long prow = cur.row0 + tok;
 #pragma unroll 1
         for (int c = 0; c < AD / 64; ++c) {
           const int col = half * (AD / 2) + c * 32;
@@ -662,17 +697,17 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
             for (int q = 0; q < 8; ++q) po[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
           } else if (row_ok) {
-            const uint4* gp = reinterpret_cast<const uint4*>(a.qkvg + prow * qc + (a.H + 2 * a.Hkv + h) * AD + col);
             uint4* op = reinterpret_cast<uint4*>(a.out + prow * (a.H * AD) + h * AD + col);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const uint4 gv = __ldg(gp + q);
+              const uint4 gv = gates[q];
+              if (c == 0) gates[q] = __ldg(gp + 4 + q);
               const uint32_t gw[4] = {gv.x, gv.y, gv.z, gv.w};
               uint32_t ow[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                ow[e] = pack_bf16x2(o[q * 8 + 2 * e] * inv_l * sigmoid_f(bf16_lo(gw[e])),
-                                    o[q * 8 + 2 * e + 1] * inv_l * sigmoid_f(bf16_hi(gw[e])));
+                ow[e] = pack_bf16x2(o[q * 8 + 2 * e] * inv_l * sigmoid_fast(bf16_lo(gw[e])),
+                                    o[q * 8 + 2 * e + 1] * inv_l * sigmoid_fast(bf16_hi(gw[e])));
               op[q] = make_uint4(ow[0], ow[1], ow[2], ow[3]);
             }
           }
@@ -749,8 +784,8 @@ __global__ void __launch_bounds__(256) paged_attn_join_kernel(Args a) {
     }
     const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
     uint2 r;
-    r.x = pack_bf16x2(o[0] * inv * sigmoid_f(bf16_lo(g.x)), o[1] * inv * sigmoid_f(bf16_hi(g.x)));
-    r.y = pack_bf16x2(o[2] * inv * sigmoid_f(bf16_lo(g.y)), o[3] * inv * sigmoid_f(bf16_hi(g.y)));
+    r.x = pack_bf16x2(o[0] * inv * sigmoid_fast(bf16_lo(g.x)), o[1] * inv * sigmoid_fast(bf16_hi(g.x)));
+    r.y = pack_bf16x2(o[2] * inv * sigmoid_fast(bf16_lo(g.y)), o[3] * inv * sigmoid_fast(bf16_hi(g.y)));
     *reinterpret_cast<uint2*>(a.out + prow * (a.H * AD) + h * AD + lane * 4) = r;
   }
 }
