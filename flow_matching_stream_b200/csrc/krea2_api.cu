@@ -863,7 +863,9 @@ int krea2_paged_kv_append(const Krea2Dims* dims, const Krea2PagedBatch* batch, i
   int rc = check_dims(dims, dtype);
   if (rc || (rc = check_batch(batch))) return rc;
   if (!qkvg || !k_norm_w || !cos || !sin) return set_error(KREA2_ERR_ARG, "NULL pointer");
-  if (reinterpret_cast<uintptr_t>(qkvg) & 15) return set_error(KREA2_ERR_ARG, "qkvg must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(qkvg) | reinterpret_cast<uintptr_t>(k_norm_w) | reinterpret_cast<uintptr_t>(cos) |
+       reinterpret_cast<uintptr_t>(sin)) & 15)
+    return set_error(KREA2_ERR_ARG, "qkvg, k_norm_w, cos and sin must be 16-byte aligned");
   return launch_paged_append(*batch, dims, dtype == KREA2_BF16, qkvg, k_norm_w, cos, sin, as_stream(stream));
 }
 
@@ -880,8 +882,9 @@ int krea2_gqa_attention_paged(const Krea2Dims* dims, const Krea2PagedBatch* batc
   if (rc || (rc = check_batch(batch))) return rc;
   if (T < 0) return set_error(KREA2_ERR_ARG, "text length must be >= 0");
   if (!qkvg || !q_norm_w || !cos || !sin || !out) return set_error(KREA2_ERR_ARG, "NULL pointer");
-  if ((reinterpret_cast<uintptr_t>(qkvg) | reinterpret_cast<uintptr_t>(out)) & 15)
-    return set_error(KREA2_ERR_ARG, "qkvg and out must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(qkvg) | reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(q_norm_w) |
+       reinterpret_cast<uintptr_t>(cos) | reinterpret_cast<uintptr_t>(sin)) & 15)
+    return set_error(KREA2_ERR_ARG, "qkvg, out, q_norm_w, cos and sin must be 16-byte aligned");
   const size_t need = krea2_paged_attention_workspace_size(dims, batch, dtype);
   if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255)))
     return set_error(KREA2_ERR_WORKSPACE, "workspace must be non-NULL and 256-byte aligned");

@@ -51,86 +51,102 @@ __global__ void __launch_bounds__(256) lora_down_simt_kernel(Krea2Lora l, int M,
   if (lane == 0) t[(long)row * l.rank + j] = s;
 }
 
-constexpr int LBM = 64, LBN = 128, LBK = 16;
-
-// 64 x 128 tiles; thread (tx, ty) holds rows ty*4.. and columns tx*4.. of both 64-column halves, so that
-// a SwiGLU tile's gate and up columns of one output meet in one thread.
-template <int EPI>
-__global__ void __launch_bounds__(256) lora_linear_simt_kernel(Krea2Lora l, int M, int N, int K,
-                                                               const float* __restrict__ A, const float* __restrict__ W,
-                                                               const float* __restrict__ t, void* out,
-                                                               const float* __restrict__ gate, int rows_per_batch,
-                                                               long long gate_stride) {
-  __shared__ float As[LBK][LBM + 4];
-  __shared__ float Ws[LBK][LBN + 4];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int m0 = blockIdx.y * LBM, n0 = blockIdx.x * LBN;
+// TM x TN tiles of the output. A tile's columns are TN / 2 neighbours of the first and the same of the second half
+// of a 128-column group, so that a SwiGLU output's gate and up columns meet in one thread; a thread holds RM rows
+// and HC columns of each half.
+template <int TM, int TN, int RM, int HC, int BK, int EPI>
+__global__ void __launch_bounds__((TM / RM) * (TN / (2 * HC)))
+    lora_linear_simt_kernel(Krea2Lora l, int M, int N, int K, const float* __restrict__ A, const float* __restrict__ W,
+                            const float* __restrict__ t, void* out, const float* __restrict__ gate, int rows_per_batch,
+                            long long gate_stride) {
+  constexpr int TX = TN / (2 * HC), NT = (TM / RM) * TX, HALF = TN / 2, PER_GROUP = 128 / TN;
+  constexpr int LA = TM * BK / NT, LW = TN * BK / NT;
+  __shared__ float As[BK][TM + 1];
+  __shared__ float Ws[BK][TN + 1];
+  const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
+  const int m0 = blockIdx.y * TM, c0 = (blockIdx.x / PER_GROUP) * 128 + (blockIdx.x % PER_GROUP) * HALF;
+  auto col = [&](int c) { return c0 + (c % HALF) + (c / HALF) * 64; };  // of the tile's column c
   const int used = used_rows(l, M);
   if (m0 >= used) return;
-  float acc[4][8];
+  float acc[RM][2 * HC];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < RM; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
-  for (int k0 = 0; k0 < K; k0 += LBK) {
-    for (int i = threadIdx.x; i < LBM * LBK; i += 256) {
-      const int r = i / LBK, k = i % LBK;
-      As[k][r] = (m0 + r < used && k0 + k < K) ? (A[(long)(m0 + r) * K + k0 + k]) : 0.f;
+    for (int j = 0; j < 2 * HC; ++j) acc[i][j] = 0.f;
+  float ra[LA], rw[LW];  // the next K step's elements, on their way while this one is multiplied
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int i = 0; i < LA; ++i) {
+      const int e = threadIdx.x + i * NT, r = m0 + e / BK, k = k0 + e % BK;
+      ra[i] = (r < used && k < K) ? A[(long long)r * K + k] : 0.f;
     }
-    for (int i = threadIdx.x; i < LBN * LBK; i += 256) {
-      const int r = i / LBK, k = i % LBK;
-      Ws[k][r] = (n0 + r < N && k0 + k < K) ? (W[(long)(n0 + r) * K + k0 + k]) : 0.f;
+#pragma unroll
+    for (int i = 0; i < LW; ++i) {
+      const int e = threadIdx.x + i * NT, n = col(e / BK), k = k0 + e % BK;
+      rw[i] = (n < N && k < K) ? W[(long long)n * K + k] : 0.f;
     }
+  };
+  load(0);
+  for (int k0 = 0; k0 < K; k0 += BK) {
+#pragma unroll
+    for (int i = 0; i < LA; ++i) As[(threadIdx.x + i * NT) % BK][(threadIdx.x + i * NT) / BK] = ra[i];
+#pragma unroll
+    for (int i = 0; i < LW; ++i) Ws[(threadIdx.x + i * NT) % BK][(threadIdx.x + i * NT) / BK] = rw[i];
     __syncthreads();
+    if (k0 + BK < K) load(k0 + BK);
+#pragma unroll 16
+    for (int k = 0; k < BK; ++k) {
+      float a[RM], w[2 * HC];
 #pragma unroll
-    for (int k = 0; k < LBK; ++k) {
-      float a[4], w[8];
+      for (int i = 0; i < RM; ++i) a[i] = As[k][ty * RM + i];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] = As[k][ty * 4 + i];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        w[j] = Ws[k][tx * 4 + j];
-        w[4 + j] = Ws[k][64 + tx * 4 + j];
+      for (int j = 0; j < HC; ++j) {
+        w[j] = Ws[k][tx * HC + j];
+        w[HC + j] = Ws[k][HALF + tx * HC + j];
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < RM; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i][j] += a[i] * w[j];
+        for (int j = 0; j < 2 * HC; ++j) acc[i][j] += a[i] * w[j];
     }
     __syncthreads();
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = m0 + ty * 4 + i;
+  for (int i = 0; i < RM; ++i) {
+    const int r = m0 + ty * RM + i;
     if (r >= used) continue;
     const int id = adapter_of_row(l, r);
-    if (id >= 0) {
-      const float* tr = t + (long)r * l.rank;
-      const float* up = reinterpret_cast<const float*>(l.up) + (long)id * N * l.rank;
+    if (id >= 0) {  // rank is a multiple of 8: whole 16-byte loads
+      const float4* tr = reinterpret_cast<const float4*>(t + (long long)r * l.rank);
+      const float* up = reinterpret_cast<const float*>(l.up) + (long long)id * N * l.rank;
 #pragma unroll
-      for (int jj = 0; jj < 8; ++jj) {
-        const int c = n0 + (jj < 4 ? tx * 4 + jj : 60 + tx * 4 + jj);
+      for (int j = 0; j < 2 * HC; ++j) {
+        const int c = col(j < HC ? tx * HC + j : HALF + tx * HC + j - HC);
         if (c >= N) continue;
-        const float* u = up + (long)c * l.rank;
-        for (int k = 0; k < l.rank; ++k) acc[i][jj] += tr[k] * (u[k]);
+        const float4* u = reinterpret_cast<const float4*>(up + (long long)c * l.rank);
+        for (int k = 0; k < l.rank / 4; ++k) {
+          const float4 x = tr[k], y = u[k];
+          acc[i][j] += x.x * y.x;
+          acc[i][j] += x.y * y.y;
+          acc[i][j] += x.z * y.z;
+          acc[i][j] += x.w * y.w;
+        }
       }
     }
     if constexpr (EPI == EPI_SWIGLU) {
-      float* o = reinterpret_cast<float*>(out) + (long)r * (N / 2) + blockIdx.x * 64;
+      float* o = reinterpret_cast<float*>(out) + (long long)r * (N / 2) + c0 / 128 * 64 + c0 % 128;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        o[tx * 4 + j] = acc[i][j] / (1.f + expf(-acc[i][j])) * acc[i][4 + j];
-      }
+      for (int j = 0; j < HC; ++j) o[tx * HC + j] = acc[i][j] / (1.f + expf(-acc[i][j])) * acc[i][HC + j];
     } else {
 #pragma unroll
-      for (int jj = 0; jj < 8; ++jj) {
-        const int c = n0 + (jj < 4 ? tx * 4 + jj : 60 + tx * 4 + jj);
+      for (int j = 0; j < 2 * HC; ++j) {
+        const int c = col(j < HC ? tx * HC + j : HALF + tx * HC + j - HC);
         if (c >= N) continue;
         if constexpr (EPI == EPI_RESID) {
           const int b = rows_per_batch > 0 ? r / rows_per_batch : request_of_row(l.row_start, l.R, r);
-          reinterpret_cast<float*>(out)[(long)r * N + c] += gate[(long)b * gate_stride + c] * acc[i][jj];
+          reinterpret_cast<float*>(out)[(long long)r * N + c] += gate[(long long)b * gate_stride + c] * acc[i][j];
         } else {
-          reinterpret_cast<float*>(out)[(long)r * N + c] = acc[i][jj];
+          reinterpret_cast<float*>(out)[(long long)r * N + c] = acc[i][j];
         }
       }
     }
@@ -151,14 +167,26 @@ int lora_simt(int epi, const LoraLinearArgs& a, const Krea2Lora& l, float* t, cu
   lora_down_simt_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(l, a.M, a.K, A, t);
   int rc = check_launch("lora_down");
   if (rc) return rc;
-  dim3 grid((a.N + LBN - 1) / LBN, (a.M + LBM - 1) / LBM);
-  if (grid.y > 65535) return set_error(KREA2_ERR_UNSUPPORTED, "more than %d rows", 65535 * LBM);
+  // 64 x 128 tiles, or 16 x 32 where those would leave most SMs without one (73 x 640, K 256: 10 large tiles take
+  // 55 us, 100 small ones 8 us; from two large tiles per SM on the large ones' reuse wins)
+  const int groups = (a.N + 127) / 128;
+  const bool small = (long long)groups * ((a.M + 63) / 64) < 2L * num_sms();
+  const dim3 grid(small ? groups * 4 : groups, small ? (a.M + 15) / 16 : (a.M + 63) / 64);
+  if (grid.y > 65535) return set_error(KREA2_ERR_UNSUPPORTED, "more than %d rows", 65535 * 64);
 #define KREA2_LORA(E)                                                                                            \
-  lora_linear_simt_kernel<E><<<grid, 256, 0, stream>>>(l, a.M, a.N, a.K, A, W, t, a.out, a.gate, a.rows_per_batch, \
-                                                       a.gate_stride)
-  if (epi == EPI_STORE) KREA2_LORA(EPI_STORE);
-  else if (epi == EPI_SWIGLU) KREA2_LORA(EPI_SWIGLU);
-  else KREA2_LORA(EPI_RESID);
+  if (small)                                                                                                     \
+    lora_linear_simt_kernel<16, 32, 1, 2, 64, E><<<grid, 128, 0, stream>>>(l, a.M, a.N, a.K, A, W, t, a.out, a.gate, \
+                                                                          a.rows_per_batch, a.gate_stride);      \
+  else                                                                                                           \
+    lora_linear_simt_kernel<64, 128, 4, 4, 16, E><<<grid, 256, 0, stream>>>(l, a.M, a.N, a.K, A, W, t, a.out, a.gate, \
+                                                                           a.rows_per_batch, a.gate_stride)
+  if (epi == EPI_STORE) {
+    KREA2_LORA(EPI_STORE);
+  } else if (epi == EPI_SWIGLU) {
+    KREA2_LORA(EPI_SWIGLU);
+  } else {
+    KREA2_LORA(EPI_RESID);
+  }
 #undef KREA2_LORA
   return check_launch("lora_linear");
 }

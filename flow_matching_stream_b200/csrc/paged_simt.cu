@@ -63,7 +63,14 @@ __device__ __forceinline__ void load_f(const T* p, float* v) {
   }
 }
 
-// One warp per (row, KV head); each lane holds D / 32 columns (whole rotation pairs).
+template <typename T, int E>
+struct alignas(sizeof(T) * E) Pack {
+  T v[E];
+};
+
+// One warp per (row, four KV heads), bound by its bytes: k and v of the four heads are on their way (8 or 16 bytes a
+// lane) while the row's request and page are looked up. Each lane holds D / 32 columns (whole rotation pairs).
+constexpr int APPEND_HEADS = 4;
 template <typename T, int D>
 __global__ void __launch_bounds__(256) paged_append_kernel(PagedArgs p, const T* __restrict__ qkvg, int H, int Hkv,
                                                            float eps, const float* __restrict__ kw,
@@ -71,41 +78,58 @@ __global__ void __launch_bounds__(256) paged_append_kernel(PagedArgs p, const T*
                                                            T* __restrict__ kp, T* __restrict__ vp) {
   check_requests(p);
   constexpr int E = D / 32;
+  using V = Pack<T, E>;
+  using F = Pack<float, E>;
+  using F2 = Pack<float, E / 2>;
+  const int parts = (Hkv + APPEND_HEADS - 1) / APPEND_HEADS;
   const long gw = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  if (gw >= (long)p.M * Hkv) return;
-  const int row = (int)(gw / Hkv), hh = (int)(gw % Hkv);
+  const int row = (int)(gw / parts), h0 = (int)(gw % parts) * APPEND_HEADS;
+  // rows behind the last request are not read; a bad end is caught by the look-up below
+  if (row >= p.M || row >= __ldg(p.q_start + p.R)) return;
+  const T* x = qkvg + (long)row * (2L * (H + Hkv) * D);
+  V kr[APPEND_HEADS], vr[APPEND_HEADS];
+#pragma unroll
+  for (int i = 0; i < APPEND_HEADS; ++i) {
+    const int hh = min(h0 + i, Hkv - 1);
+    kr[i] = *reinterpret_cast<const V*>(x + (long)(H + hh) * D + lane * E);
+    vr[i] = *reinterpret_cast<const V*>(x + (long)(H + Hkv + hh) * D + lane * E);
+  }
+  const F w = *reinterpret_cast<const F*>(kw + lane * E);
+  const F2 c = *reinterpret_cast<const F2*>(cs + (long)row * (D / 2) + lane * (E / 2));
+  const F2 sv = *reinterpret_cast<const F2*>(sn + (long)row * (D / 2) + lane * (E / 2));
   RequestRows q;
   bool bad;
   const int r = checked_request_of_row(p, row, &q, &bad);
-  if (r < 0) return;  // behind the last request, or a request that check_requests reports
+  if (r < 0) return;  // a request that check_requests reports
   const int t = q.L - q.n + (row - q.row0);
   const int page = p.page_table[(long)r * p.max_pages + t / p.page_size];
   if (page < 0 || page >= p.num_pages) {
     report_bad_batch();
     return;
   }
-  const T* x = qkvg + (long)row * (2L * (H + Hkv) * D);
-  const T* xk = x + (long)(H + hh) * D + lane * E;
-  const T* xv = x + (long)(H + Hkv + hh) * D + lane * E;
-  float v[E], ss = 0.f;
+  const long d = ((long)page * p.page_size + t % p.page_size) * (long)(Hkv * D) + lane * E;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    v[e] = to_f(xk[e]);
-    ss += v[e] * v[e];
-  }
-  const float rs = rsqrtf(warp_sum(ss) / (float)D + eps);
-  const long d = ((long)page * p.page_size + t % p.page_size) * (long)(Hkv * D) + (long)hh * D + lane * E;
+  for (int i = 0; i < APPEND_HEADS; ++i) {
+    float v[E], ss = 0.f;
 #pragma unroll
-  for (int e = 0; e < E; e += 2) {
-    const long a = (long)row * (D / 2) + lane * (E / 2) + e / 2;
-    // the grouping of the contiguous cache's append, so that both give the same bits
-    const float x0 = v[e] * (rs * (1.f + kw[lane * E + e])), x1 = v[e + 1] * (rs * (1.f + kw[lane * E + e + 1]));
-    const float c = cs[a], s = sn[a];
-    kp[d + e] = from_f<T>(x0 * c - x1 * s);
-    kp[d + e + 1] = from_f<T>(x1 * c + x0 * s);
-    vp[d + e] = xv[e];
-    vp[d + e + 1] = xv[e + 1];
+    for (int e = 0; e < E; ++e) {
+      v[e] = to_f(kr[i].v[e]);
+      ss += v[e] * v[e];
+    }
+    const float rs = rsqrtf(warp_sum(ss) / (float)D + eps);
+    V o;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      // the grouping and the fused products of the contiguous cache's append, so that both give the same bits
+      const float x0 = v[e] * (rs * (1.f + w.v[e])), x1 = v[e + 1] * (rs * (1.f + w.v[e + 1]));
+      o.v[e] = from_f<T>(__fmaf_rn(x0, c.v[e / 2], -__fmul_rn(x1, sv.v[e / 2])));
+      o.v[e + 1] = from_f<T>(__fmaf_rn(x0, sv.v[e / 2], __fmul_rn(x1, c.v[e / 2])));
+    }
+    if (h0 + i < Hkv) {
+      *reinterpret_cast<V*>(kp + d + (long)(h0 + i) * D) = o;
+      *reinterpret_cast<V*>(vp + d + (long)(h0 + i) * D) = vr[i];
+    }
   }
 }
 
@@ -215,7 +239,8 @@ int check_launch(const char* what) {
 int launch_paged_append(const Krea2PagedBatch& b, const Krea2Dims* d, bool bf16, const void* qkvg, const float* kw,
                         const float* cs, const float* sn, cudaStream_t stream) {
   const PagedArgs p = args_of(b);
-  const long warps = (long)b.M * d->Hkv;
+  const long warps = (long)b.M * ((d->Hkv + APPEND_HEADS - 1) / APPEND_HEADS);
+  if ((warps + 7) / 8 > 0x7fffffffL) return set_error(KREA2_ERR_UNSUPPORTED, "too many rows x KV heads");
   const unsigned grid = (unsigned)((warps + 7) / 8);
 #define KREA2_APPEND(T, DD)                                                                                      \
   paged_append_kernel<T, DD><<<grid, 256, 0, stream>>>(p, reinterpret_cast<const T*>(qkvg), d->H, d->Hkv, d->eps, \

@@ -441,7 +441,7 @@ int krea2_paged_batch_check(const Krea2PagedBatch* batch);
 
 /* krea2_kv_cache_append for a paged batch: the keys and values of all new tokens into their pages.
  *   qkvg (M, H*D + 2*Hkv*D + H*D) raw fused projection of the new tokens; only k and v columns are
- *   read. cos, sin (M, D/2) fp32: RoPE tables of the packed rows.
+ *   read. cos, sin (M, D/2) fp32: RoPE tables of the packed rows. All 16-byte aligned, as k_norm_w.
  * bf16 and fp32, D in {64, 128}. No two new tokens may have the same slot. */
 int krea2_paged_kv_append(const Krea2Dims* dims, const Krea2PagedBatch* batch, int dtype,
                           const void* qkvg, const float* k_norm_w, const float* cos, const float* sin,
@@ -453,7 +453,7 @@ int krea2_paged_kv_append(const Krea2Dims* dims, const Krea2PagedBatch* batch, i
  *   key_end NULL: every new token reads all kv_len keys. key_end (M) int32 DEVICE: row i reads keys
  *     [0, key_end[i]) (positions in its request); a value below the token's own position + 1 is
  *     raised to it, one above kv_len is cut to it.
- *   qkvg, cos, sin as in krea2_paged_kv_append; q and gate columns are read.
+ *   qkvg, cos, sin as in krea2_paged_kv_append; q and gate columns are read. q_norm_w and out 16-byte aligned.
  *   out (M, H*D) in `dtype`: sigmoid(gate) * attention, heads merged. A token with no readable key
  *     outputs zeros.
  * Keys past kv_len and keys that text_mask removes are not used, whatever their pages hold (NaN

@@ -56,14 +56,17 @@ def test_bad_attention_arguments(K2):
     assert call(T=-1) == -1 and call(dtype=2) == -1
     for name in ("qkvg", "qw", "cos", "sin", "out"):
         assert call(**{name: None}) == -1
-    assert call(qkvg=FAKE + 8) == -1 and call(out=FAKE + 4) == -1
+    for name in ("qkvg", "out", "qw", "cos", "sin"):
+        assert call(**{name: FAKE + 8}) == -1
     if need:
         assert call(ws=None) == -2 and call(ws=FAKE + 128) == -2 and call(n=need - 1) == -2
     assert lib.krea2_gqa_attention_paged(ctypes.byref(d), None, 0, 0, FAKE, FAKE, FAKE, FAKE, None, None, FAKE, FAKE,
                                          need, None) == -1
     assert lib.krea2_paged_attention_workspace_size(ctypes.byref(d), ctypes.byref(batch(R=0)), 0) == 0
     assert lib.krea2_paged_kv_append(ctypes.byref(d), ctypes.byref(b), 0, None, FAKE, FAKE, FAKE, None) == -1
-    assert lib.krea2_paged_kv_append(ctypes.byref(d), ctypes.byref(b), 0, FAKE + 2, FAKE, FAKE, FAKE, None) == -1
+    for i in range(4):
+        at = [FAKE + 8 if i == k else FAKE for k in range(4)]
+        assert lib.krea2_paged_kv_append(ctypes.byref(d), ctypes.byref(b), 0, *at, None) == -1
     bad = K2.dims_struct(KI.FULL)
     bad.axes[0] = 30
     assert lib.krea2_paged_kv_append(ctypes.byref(bad), ctypes.byref(b), 0, FAKE, FAKE, FAKE, FAKE, None) == -1
