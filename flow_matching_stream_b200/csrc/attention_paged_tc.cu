@@ -37,7 +37,7 @@ namespace {
 
 constexpr int KT = 64;            // keys per tile
 constexpr int THREADS = 320;
-constexpr int SOFTMAX_THREADS = 256;
+constexpr int SOFTMAX_WARPS = 8;
 constexpr int KV_CHUNK = KT * 128;  // 64 keys x 64 bf16
 constexpr int KV_TILE_BYTES = 2 * KV_CHUNK;
 
@@ -202,6 +202,12 @@ __device__ __forceinline__ uint32_t used_tiles(const Args& a, int r, int L, int 
   return word;
 }
 
+// One arrival per warp: 32 lanes' arrivals on one barrier are taken one after the other.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
 template <int G, bool FEW>
 __global__ void __launch_bounds__(THREADS, 2)
     paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, Args a) {
@@ -227,9 +233,9 @@ __global__ void __launch_bounds__(THREADS, 2)
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&seg_full[s], 1);
-      mbar_init(&seg_empty[s], SOFTMAX_THREADS + 1);
+      mbar_init(&seg_empty[s], SOFTMAX_WARPS + 1);
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], SOFTMAX_THREADS);
+      mbar_init(&p_full[s], SOFTMAX_WARPS);
       mbar_init(&pv_done[s], 1);
     }
     for (int s = 0; s < STAGES; ++s) {
@@ -238,7 +244,7 @@ __global__ void __launch_bounds__(THREADS, 2)
       mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 1);
     }
-    mbar_init(&q_full, SOFTMAX_THREADS);
+    mbar_init(&q_full, SOFTMAX_WARPS);
     mbar_init(&drain_bar, 1);
     abort_flag = 0;
     fence_barrier_init();
@@ -335,7 +341,7 @@ __global__ void __launch_bounds__(THREADS, 2)
       int prev_count = 0;
       auto load_v = [&]() -> bool {
         const int st = v_st;
-        if (!__all_sync(0xffffffffu, mbar_wait(&v_empty[st], v_ph ^ 1, abort))) return false;
+        if (!__all_sync(0xffffffffu, mbar_wait(FEW ? &v_empty[st] : &pv_done[st], v_ph ^ 1, abort))) return false;
         uint8_t* vd = base + OFF_V + st * KV_TILE_BYTES;
         if (lane == 0) mbar_arrive_expect_tx(&v_full[st], prev_count * a.group * (2 * AD));
         __syncwarp();
@@ -376,7 +382,9 @@ __global__ void __launch_bounds__(THREADS, 2)
         const int page = __shfl_sync(0xffffffffu, my_page, src), slot_in = __shfl_sync(0xffffffffu, my_slot, src);
         const bool has = (lane >> 1) < count;
         const int st = k_st;
-        if (!__all_sync(0xffffffffu, mbar_wait(&k_empty[st], k_ph ^ 1, abort))) return false;
+        // With two stages tile i's are those of tile i - 2, whose products complete s_full and pv_done (and tile i's
+        // own complete them next, so the phase is never missed); a third stage takes barriers of its own.
+        if (!__all_sync(0xffffffffu, mbar_wait(FEW ? &k_empty[st] : &s_full[st], k_ph ^ 1, abort))) return false;
         uint8_t* kd = base + OFF_K + st * KV_TILE_BYTES;
         if (lane == 0) {
           tile_of[it % TILE_RING] = t;
@@ -435,7 +443,10 @@ __global__ void __launch_bounds__(THREADS, 2)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
+    // ---- MMAs. The whole warp runs along, so that descriptors and loop counters are warp-uniform (they live in
+    // uniform registers, where the MMA takes them from); one elected lane issues.
+    {
+      const bool leader = elect_one();
       const uint64_t dq0 = smem_desc_sw128(smem_u32(base), 16, 1024);
       const uint64_t dk0 = smem_desc_sw128(smem_u32(base + OFF_K), 16, 1024);
       const uint64_t dv0 = smem_desc_sw128(smem_u32(base + OFF_V), KV_CHUNK, 1024);
@@ -450,57 +461,64 @@ __global__ void __launch_bounds__(THREADS, 2)
         }
       };
       for (int seg = 0; ok; ++seg) {
-        if (!mbar_wait(&seg_full[seg & 1], (seg >> 1) & 1, abort)) break;
+        if (!__all_sync(0xffffffffu, mbar_wait(&seg_full[seg & 1], (seg >> 1) & 1, abort))) break;
         const int n = segs[seg & 1].n, tiles = segs[seg & 1].tiles;
-        mbar_arrive(&seg_empty[seg & 1]);
+        __syncwarp();
+        if (leader) mbar_arrive(&seg_empty[seg & 1]);
         if (n < 0) break;
         if (tiles == 0) continue;  // no product, and no arrival on q_full
-        if (!mbar_wait(&q_full, queries++ & 1, abort)) break;
+        if (!__all_sync(0xffffffffu, mbar_wait(&q_full, queries++ & 1, abort))) break;
         tc_fence_after();
+        // Step i issues P V of tile i - 2, then Q K of tile i into the scores that P overlaid. Of the waits only the one
+        // for P is not long over, so it comes last; s_full is committed first: from a tile's P to the scores two tiles
+        // on and their softmax is the loop that sets the pace.
         const int first = it;
-        auto issue_pv = [&](int i) -> bool {
-          const int sb = i & 1;
-          if (!mbar_wait2(&p_full[sb], (i >> 1) & 1, &v_full[v_st], v_ph, abort)) return false;
-          tc_fence_after();
+        auto wait_v = [&]() { return __all_sync(0xffffffffu, mbar_wait(&v_full[v_st], v_ph, abort)); };
+        auto wait_p = [&](int i) { return __all_sync(0xffffffffu, mbar_wait(&p_full[i & 1], (i >> 1) & 1, abort)); };
+        auto issue_pv = [&](int i) {  // the leader's
           const uint64_t dv = dv0 + (uint64_t)(v_st * (KV_TILE_BYTES >> 4));
-          const uint32_t pt = tmem + sb * KT;
+          const uint32_t pt = tmem + (i & 1) * KT;
 #pragma unroll
           for (int kk = 0; kk < KT / 16; ++kk)
             tc_mma_bf16_ts(tmem + O_COL, pt + kk * 8, dv + (uint64_t)(kk * 16 * 128 >> 4), IDESC_PV,
                            (i > first || kk > 0) ? 1u : 0u);
-          tc_commit(&pv_done[sb]);
-          tc_commit(&v_empty[v_st]);
-          step(v_st, v_ph);
-          return true;
         };
-        for (int i = 0; i < tiles; ++i, ++it) {
-          const int sb = it & 1;
-          if (!mbar_wait(&k_full[k_st], k_ph, abort)) {
-            ok = false;
-            break;
-          }
+        auto commit_pv = [&](int i) {
+          tc_commit(&pv_done[i & 1]);
+          if constexpr (FEW) tc_commit(&v_empty[v_st]);
+        };
+        const int end = first + tiles;
+        for (; it < end + 2; ++it) {
+          const bool qk = it < end, pv = it - 2 >= first;
+          if (qk && !__all_sync(0xffffffffu, mbar_wait(&k_full[k_st], k_ph, abort))) ok = false;
+          if (ok && pv && !(wait_v() && wait_p(it - 2))) ok = false;
+          if (!ok) break;
           tc_fence_after();
-          const uint64_t dk = dk0 + (uint64_t)(k_st * (KV_TILE_BYTES >> 4));
-          const uint32_t d_s = tmem + sb * KT;
+          if (leader) {
+            if (pv) issue_pv(it - 2);
+            if (qk) {
+              const uint64_t dk = dk0 + (uint64_t)(k_st * (KV_TILE_BYTES >> 4));
+              const uint32_t d_s = tmem + (it & 1) * KT;
 #pragma unroll
-          for (int kk = 0; kk < AD / 16; ++kk) {
-            const uint32_t qo = (kk >> 2) * Q_CHUNK + (kk & 3) * 32;
-            const uint32_t ko = (kk >> 2) * KV_CHUNK + (kk & 3) * 32;
-            tc_mma_bf16(d_s, dq0 + (uint64_t)(qo >> 4), dk + (uint64_t)(ko >> 4), IDESC_QK, kk > 0 ? 1u : 0u);
+              for (int kk = 0; kk < AD / 16; ++kk) {
+                const uint32_t qo = (kk >> 2) * Q_CHUNK + (kk & 3) * 32;
+                const uint32_t ko = (kk >> 2) * KV_CHUNK + (kk & 3) * 32;
+                tc_mma_bf16(d_s, dq0 + (uint64_t)(qo >> 4), dk + (uint64_t)(ko >> 4), IDESC_QK, kk > 0 ? 1u : 0u);
+              }
+              tc_commit(&s_full[it & 1]);
+              if constexpr (FEW) tc_commit(&k_empty[k_st]);
+            }
+            if (pv) commit_pv(it - 2);
           }
+          __syncwarp();
           issued = true;
-          tc_commit(&s_full[sb]);
-          tc_commit(&k_empty[k_st]);
-          step(k_st, k_ph);
-          if (i >= 1 && !issue_pv(it - 1)) {
-            ok = false;
-            break;
-          }
+          if (qk) step(k_st, k_ph);
+          if (pv) step(v_st, v_ph);
         }
-        if (ok) ok = issue_pv(it - 1);
+        it = end;
       }
       if (*abort && issued) {
-        tc_commit(&drain_bar);
+        if (leader) tc_commit(&drain_bar);
         mbar_wait_drain(&drain_bar, 0);
       }
     }
@@ -556,7 +574,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         }
       }
       fence_proxy_async_smem();
-      mbar_arrive(&q_full);
+      warp_arrive(&q_full, lane);
       return true;
     };
 
@@ -656,7 +674,7 @@ __global__ void __launch_bounds__(THREADS, 2)
           tmem_wait_st();
         }
         tc_fence_before();
-        mbar_arrive(&p_full[sb]);
+        warp_arrive(&p_full[sb], lane);
       }
       if (!ok) break;
       // the last s_full was the last use of Q: the next segment's queries go in, and its first product
@@ -719,7 +737,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         }
       }
       tc_fence_before();
-      mbar_arrive(&seg_empty[(seg - 1) & 1]);
+      warp_arrive(&seg_empty[(seg - 1) & 1], lane);
       ok = more;
     }
   }
