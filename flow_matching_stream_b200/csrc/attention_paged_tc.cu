@@ -5,22 +5,24 @@
 // Bound: the tensor cores and the exponentials for many new tokens (4 D H operations a token and key),
 // reading K and V once (512 bytes a key and KV head) for few.
 //
-// An item is (request, KV head, 128 / G new tokens): its 128 MMA rows are G query heads of 128 / G
-// tokens, row = token * G + head, so that few tokens fill whole warps and leave the others idle. Work is
-// cut into key tiles of 64. Every CTA (two per SM, all resident) takes
+// An item is (request, KV head, 256 / G new tokens): two teams with 128 MMA rows each, row = token * G + head,
+// so that few tokens fill whole warps and leave the others idle. The teams share the item's K and V tiles in
+// shared memory; with one team of 128 rows per tile (two CTAs per SM) the SMs took 7.9 TB/s of K and V from L2.
+// Work is cut into key tiles of 64. Every CTA (all resident) takes
 //   * whole items in turn, as many rounds as every CTA gets one item of a request: neighbours work on
 //     the same K and V at the same time;
 //   * an equal share of the key tiles of what is left, cut without regard to items. A cut item's parts
 //     (unnormalised O, row maximum and sum, fp32) go to the workspace, and a second kernel joins them in
 //     key order. One new token over a long cache is spread over all SMs this way.
+// Batches of about one new token per request have items of one team with 16 rows, two CTAs per SM.
 //
 // Roles as in attention_tc.cu, but the CTA runs through segments (an item or a part of one):
-//   warp 0      cuts the work into segments and publishes them, looks up pages, loads K and V tiles by
-//               TMA, one box per page and tile (per 16, 32 or 64 keys), into a 2-stage ring
-//   warp 1      S = Q Kᵀ into one of two TMEM buffers, O += P V with P in TMEM
-//   warps 2..9  normalise and rotate a segment's queries into shared memory, softmax, output. Where keys
-//               of a tile are masked or lie behind the request's last key, they clear those rows of V in
-//               shared memory, so that whatever the page holds there meets no probability of zero.
+//   warp 0        cuts the work into segments and publishes them, looks up pages, loads K and V tiles by
+//                 TMA, one box per page and tile (per 16, 32 or 64 keys), into a ring
+//   one warp per team   S = Q Kᵀ into one of two TMEM buffers, O += P V with P in TMEM
+//   eight warps per team   normalise and rotate the team's queries into shared memory, softmax, output. Where
+//                 keys of a tile are masked or lie behind the request's last key, they clear those rows of V
+//                 in shared memory, so that whatever the page holds there meets no probability of zero.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -36,29 +38,36 @@ KREA2_DEFINE_ERROR_READER(take_device_error_paged_tc)
 namespace {
 
 constexpr int KT = 64;            // keys per tile
-constexpr int THREADS = 320;
-constexpr int SOFTMAX_WARPS = 8;
+constexpr int SOFTMAX_WARPS = 8;  // of a team
 constexpr int KV_CHUNK = KT * 128;  // 64 keys x 64 bf16
 constexpr int KV_TILE_BYTES = 2 * KV_CHUNK;
 
-// FEW: batches of about one new token per request. Items have 16 MMA rows (16 / G tokens), which leaves the
-// room of the other queries to a third K/V stage: with few rows a tile's time is that of its loads. (The MMA
-// still reads 128 rows from each chunk of Q on, K's tiles behind the 16; those accumulator rows are not used.)
+// FEW: batches of about one new token per request. With few rows a tile's time is that of its loads, and the room
+// of the other queries goes to K and V. (The MMA still reads 128 rows from each chunk of Q on, K's tiles behind the
+// 16; those accumulator rows are not used.)
+#ifndef BIG_TEAMS
+#define BIG_TEAMS 2
+#endif
 template <int G, bool FEW>
 struct Cfg {
-  static constexpr int ROWS = FEW ? 16 : 128;   // query rows of an item
-  static constexpr int QPOS = ROWS / G;
-  static constexpr int STAGES = FEW ? 3 : 2;
+  static constexpr int TEAMS = FEW ? 1 : BIG_TEAMS;
+  static constexpr int ROWS = FEW ? 16 : 128;   // query rows of a team
+  static constexpr int QPOS = TEAMS * ROWS / G;  // tokens of an item
+  static constexpr int STAGES = FEW ? 3 : TEAMS == 1 ? 2 : 5;
+  static constexpr int CTAS_PER_SM = TEAMS == 1 ? 2 : 1;
+  static constexpr int FIRST_SOFTMAX = 1 + TEAMS;  // warp number
+  static constexpr int THREADS = 32 * (1 + TEAMS + 8 * TEAMS);
   static constexpr int Q_CHUNK = ROWS * 128;    // ROWS x 64 bf16
-  static constexpr int OFF_K = 2 * Q_CHUNK;
+  static constexpr int OFF_K = TEAMS * 2 * Q_CHUNK;
   static constexpr int OFF_V = OFF_K + STAGES * KV_TILE_BYTES;
   static constexpr int SMEM_BYTES = OFF_V + STAGES * KV_TILE_BYTES + 1024;
 };
-constexpr uint32_t TMEM_COLS = 256;  // S0 [0,64), S1 [64,128), O [128,256)
+constexpr uint32_t TEAM_COLS = 256;  // TMEM of a team: S0 [0,64), S1 [64,128), O [128,256)
 constexpr uint32_t O_COL = 128;
 constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, KT, 0, 0);
 constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, AD, 0, 1);
 constexpr int MIN_SHARE = 4;         // key tiles: below that a CTA's start costs more than it shares
+constexpr int SEGMENT_COST = 4;      // what a segment's start and end cost, in tiles: items weigh that much more
 constexpr int TILE_RING = 8;         // tile numbers in flight between warp 0 and the softmax warps
 
 struct Args {
@@ -90,7 +99,10 @@ struct Join {
 struct ItemPlan {
   RequestRows q;
   int tiles, qtiles, rounds, rest;  // rest: items beyond the whole rounds
-  long long weight;                 // of the rest, in tiles (in items where items are not cut)
+  int unit;                         // weight of an item: its tiles and SEGMENT_COST (1 where items are not cut)
+  long long weight;                 // of the rest
+  // First tile of an item's part that starts at weight `at` within the item.
+  __device__ __forceinline__ int tile_at(int at) const { return min(max(at - SEGMENT_COST, 0), tiles); }
 };
 
 template <int QPOS>
@@ -103,7 +115,8 @@ __device__ __forceinline__ ItemPlan plan_of(const Args& a, int r, bool* bad) {
   const unsigned items = (unsigned)p.qtiles * (unsigned)a.Hkv;  // below 2^32: launch_paged_attn_tc checks it
   p.rounds = (int)(items / (unsigned)a.ctas);
   p.rest = (int)(items - (unsigned)p.rounds * (unsigned)a.ctas);
-  p.weight = (long long)p.rest * (a.split ? p.tiles : 1);
+  p.unit = a.split ? p.tiles + SEGMENT_COST : 1;
+  p.weight = (long long)p.rest * p.unit;
   return p;
 }
 
@@ -202,6 +215,12 @@ __device__ __forceinline__ uint32_t used_tiles(const Args& a, int r, int L, int 
   return word;
 }
 
+// The whole warp's wait; the usual case, a phase long complete, is one test and one vote.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
+
 // One arrival per warp: 32 lanes' arrivals on one barrier are taken one after the other.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();
@@ -209,16 +228,17 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
 }
 
 template <int G, bool FEW>
-__global__ void __launch_bounds__(THREADS, 2)
+__global__ void __launch_bounds__(Cfg<G, FEW>::THREADS, Cfg<G, FEW>::CTAS_PER_SM)
     paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, Args a) {
   using C = Cfg<G, FEW>;
-  constexpr int QPOS = C::QPOS, STAGES = C::STAGES, Q_CHUNK = C::Q_CHUNK, OFF_K = C::OFF_K, OFF_V = C::OFF_V;
+  constexpr int TEAMS = C::TEAMS, ROWS = C::ROWS, QPOS = C::QPOS, STAGES = C::STAGES, THREADS = C::THREADS;
+  constexpr int Q_CHUNK = C::Q_CHUNK, OFF_K = C::OFF_K, OFF_V = C::OFF_V, FIRST_SOFTMAX = C::FIRST_SOFTMAX;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t seg_full[2], seg_empty[2];
-  __shared__ __align__(8) uint64_t q_full;
+  __shared__ __align__(8) uint64_t q_full[TEAMS];
   __shared__ __align__(8) uint64_t k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES];
-  __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done[2];
-  __shared__ __align__(8) uint64_t drain_bar;
+  __shared__ __align__(8) uint64_t s_full[TEAMS][2], p_full[TEAMS][2], pv_done[TEAMS][2];
+  __shared__ __align__(8) uint64_t drain_bar[TEAMS];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ Segment segs[2];
@@ -233,32 +253,36 @@ __global__ void __launch_bounds__(THREADS, 2)
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&seg_full[s], 1);
-      mbar_init(&seg_empty[s], SOFTMAX_WARPS + 1);
-      mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], SOFTMAX_WARPS);
-      mbar_init(&pv_done[s], 1);
+      mbar_init(&seg_empty[s], TEAMS * (SOFTMAX_WARPS + 1));
     }
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&k_full[s], 1);
-      mbar_init(&k_empty[s], 1);
+      mbar_init(&k_empty[s], TEAMS);
       mbar_init(&v_full[s], 1);
-      mbar_init(&v_empty[s], 1);
+      mbar_init(&v_empty[s], TEAMS);
     }
-    mbar_init(&q_full, SOFTMAX_WARPS);
-    mbar_init(&drain_bar, 1);
+    for (int t = 0; t < TEAMS; ++t) {
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(&s_full[t][s], 1);
+        mbar_init(&p_full[t][s], SOFTMAX_WARPS);
+        mbar_init(&pv_done[t][s], 1);
+      }
+      mbar_init(&q_full[t], SOFTMAX_WARPS);
+      mbar_init(&drain_bar[t], 1);
+    }
     abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
-  if (warp == 1) tmem_alloc(&tmem_slot, TMEM_COLS);
+  if (warp == 1) tmem_alloc(&tmem_slot, TEAMS * TEAM_COLS);
   const Place place = find_place<QPOS>(a, blockIdx.x, &place_sh, warp_sums);
   // the join kernel behind this grid may be made ready (it waits for this grid's end)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem_base = tmem_slot;
   volatile int* abort = &abort_flag;
 
   if (warp == 0) {
@@ -280,7 +304,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     bool ok = true;
 
     auto publish = [&](const Segment& s) -> bool {
-      if (!__all_sync(0xffffffffu, mbar_wait(&seg_empty[seg & 1], ((seg >> 1) & 1) ^ 1, abort))) return false;
+      if (!warp_wait(&seg_empty[seg & 1], ((seg >> 1) & 1) ^ 1, abort)) return false;
       if (lane == 0) {
         segs[seg & 1] = s;
         mbar_arrive(&seg_full[seg & 1]);
@@ -341,7 +365,7 @@ __global__ void __launch_bounds__(THREADS, 2)
       int prev_count = 0;
       auto load_v = [&]() -> bool {
         const int st = v_st;
-        if (!__all_sync(0xffffffffu, mbar_wait(FEW ? &v_empty[st] : &pv_done[st], v_ph ^ 1, abort))) return false;
+        if (!warp_wait(&v_empty[st], v_ph ^ 1, abort)) return false;
         uint8_t* vd = base + OFF_V + st * KV_TILE_BYTES;
         if (lane == 0) mbar_arrive_expect_tx(&v_full[st], prev_count * a.group * (2 * AD));
         __syncwarp();
@@ -382,12 +406,12 @@ __global__ void __launch_bounds__(THREADS, 2)
         const int page = __shfl_sync(0xffffffffu, my_page, src), slot_in = __shfl_sync(0xffffffffu, my_slot, src);
         const bool has = (lane >> 1) < count;
         const int st = k_st;
-        // With two stages tile i's are those of tile i - 2, whose products complete s_full and pv_done (and tile i's
-        // own complete them next, so the phase is never missed); a third stage takes barriers of its own.
-        if (!__all_sync(0xffffffffu, mbar_wait(FEW ? &k_empty[st] : &s_full[st], k_ph ^ 1, abort))) return false;
+        if (!warp_wait(&k_empty[st], k_ph ^ 1, abort)) return false;
         uint8_t* kd = base + OFF_K + st * KV_TILE_BYTES;
         if (lane == 0) {
-          tile_of[it % TILE_RING] = t;
+          // bit 0: keys of the tile may be unused, bit 1: rows end inside it
+          const int k0 = t * KT;
+          tile_of[it % TILE_RING] = k0 | ((a.text_mask && k0 < a.T) || k0 + KT > s.L ? 1 : 0) | (k0 + KT > s.kmin ? 2 : 0);
           mbar_arrive_expect_tx(&k_full[st], count * a.group * (2 * AD));
         }
         __syncwarp();
@@ -421,13 +445,18 @@ __global__ void __launch_bounds__(THREADS, 2)
     for (int r = place.r; r < a.b.R && left > 0 && ok; ++r, off = 0) {
       bool bad;
       const ItemPlan p = plan_of<QPOS>(a, r, &bad);
-      const int unit = a.split ? p.tiles : 1;  // weight of an item
       while (off < p.weight && left > 0 && ok) {
-        const int item = p.rounds * a.ctas + (int)(off / unit), from = (int)(off % unit);
-        const int len = (int)min((long long)(unit - from), left);
-        // a part that does not start its item is the CTA's first, one that does not end it its last
-        const int slot = len == unit ? -1 : 2 * blockIdx.x + (from == 0 ? 1 : 0);
-        ok = a.split ? run_item(p, r, item, from, from + len, slot) : run_item(p, r, item, 0, p.tiles, -1);
+        const int nth = (int)(off / p.unit), at = (int)(off - (long long)nth * p.unit);
+        const int item = p.rounds * a.ctas + nth;
+        const int len = (int)min((long long)(p.unit - at), left);
+        if (a.split) {
+          const int from = p.tile_at(at), to = at + len == p.unit ? p.tiles : p.tile_at(at + len);
+          // a part that does not start its item is the CTA's first, one that does not end it its last
+          const int slot = from == 0 && to == p.tiles ? -1 : 2 * blockIdx.x + (from == 0 ? 1 : 0);
+          if (from < to) ok = run_item(p, r, item, from, to, slot);
+        } else {
+          ok = run_item(p, r, item, 0, p.tiles, -1);
+        }
         off += len;
         left -= len;
       }
@@ -442,107 +471,123 @@ __global__ void __launch_bounds__(THREADS, 2)
       v_fills.drain(v_full, STAGES);
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // ---- MMAs. The whole warp runs along, so that descriptors and loop counters are warp-uniform (they live in
-    // uniform registers, where the MMA takes them from); one elected lane issues.
-    {
-      const bool leader = elect_one();
-      const uint64_t dq0 = smem_desc_sw128(smem_u32(base), 16, 1024);
-      const uint64_t dk0 = smem_desc_sw128(smem_u32(base + OFF_K), 16, 1024);
-      const uint64_t dv0 = smem_desc_sw128(smem_u32(base + OFF_V), KV_CHUNK, 1024);
-      bool issued = false, ok = true;
-      int it = 0;
-      int queries = 0;  // segments with tiles so far
-      int k_st = 0, k_ph = 0, v_st = 0, v_ph = 0;
-      auto step = [](int& st, int& ph) {
-        if (++st == STAGES) {
-          st = 0;
-          ph ^= 1;
+  } else if (warp <= TEAMS) {
+    // ---- a team's MMAs. The whole warp runs along, so that descriptors and loop counters are warp-uniform (they
+    // live in uniform registers, where the MMA takes them from); one elected lane issues.
+    const int team = warp - 1;
+    const bool leader = elect_one();
+    const uint32_t tmem = tmem_base + team * TEAM_COLS;
+    const uint64_t dq0 = smem_desc_sw128(smem_u32(base + team * 2 * Q_CHUNK), 16, 1024);
+    const uint64_t dk0 = smem_desc_sw128(smem_u32(base + OFF_K), 16, 1024);
+    const uint64_t dv0 = smem_desc_sw128(smem_u32(base + OFF_V), KV_CHUNK, 1024);
+    bool issued = false, ok = true;
+    int it = 0;       // the team's tiles so far
+    int queries = 0;  // its segments with rows and tiles so far
+    int k_st = 0, k_ph = 0, v_st = 0, v_ph = 0;
+    auto step = [](int& st, int& ph) {
+      if (++st == STAGES) {
+        st = 0;
+        ph ^= 1;
+      }
+    };
+    auto wait = [&](uint64_t* bar, int parity) { return warp_wait(bar, parity, abort); };
+    for (int seg = 0; ok; ++seg) {
+      if (!wait(&seg_full[seg & 1], (seg >> 1) & 1)) break;
+      const int n = segs[seg & 1].n, tiles = segs[seg & 1].tiles;
+      __syncwarp();
+      if (leader) mbar_arrive(&seg_empty[seg & 1]);
+      if (n < 0) break;
+      if (n * G <= team * ROWS) {  // no rows of this team: its share of the stages is free as soon as they are full
+        for (int i = 0; i < tiles && ok; ++i) {
+          ok = wait(&k_full[k_st], k_ph);
+          if (ok && leader) mbar_arrive(&k_empty[k_st]);
+          ok = ok && wait(&v_full[v_st], v_ph);
+          if (ok && leader) mbar_arrive(&v_empty[v_st]);
+          step(k_st, k_ph);
+          step(v_st, v_ph);
         }
-      };
-      for (int seg = 0; ok; ++seg) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&seg_full[seg & 1], (seg >> 1) & 1, abort))) break;
-        const int n = segs[seg & 1].n, tiles = segs[seg & 1].tiles;
-        __syncwarp();
-        if (leader) mbar_arrive(&seg_empty[seg & 1]);
-        if (n < 0) break;
-        if (tiles == 0) continue;  // no product, and no arrival on q_full
-        if (!__all_sync(0xffffffffu, mbar_wait(&q_full, queries++ & 1, abort))) break;
-        tc_fence_after();
-        // Step i issues P V of tile i - 2, then Q K of tile i into the scores that P overlaid. Of the waits only the one
-        // for P is not long over, so it comes last; s_full is committed first: from a tile's P to the scores two tiles
-        // on and their softmax is the loop that sets the pace.
-        const int first = it;
-        auto wait_v = [&]() { return __all_sync(0xffffffffu, mbar_wait(&v_full[v_st], v_ph, abort)); };
-        auto wait_p = [&](int i) { return __all_sync(0xffffffffu, mbar_wait(&p_full[i & 1], (i >> 1) & 1, abort)); };
-        auto issue_pv = [&](int i) {  // the leader's
-          const uint64_t dv = dv0 + (uint64_t)(v_st * (KV_TILE_BYTES >> 4));
-          const uint32_t pt = tmem + (i & 1) * KT;
-#pragma unroll
-          for (int kk = 0; kk < KT / 16; ++kk)
-            tc_mma_bf16_ts(tmem + O_COL, pt + kk * 8, dv + (uint64_t)(kk * 16 * 128 >> 4), IDESC_PV,
-                           (i > first || kk > 0) ? 1u : 0u);
-        };
-        auto commit_pv = [&](int i) {
-          tc_commit(&pv_done[i & 1]);
-          if constexpr (FEW) tc_commit(&v_empty[v_st]);
-        };
-        const int end = first + tiles;
-        for (; it < end + 2; ++it) {
-          const bool qk = it < end, pv = it - 2 >= first;
-          if (qk && !__all_sync(0xffffffffu, mbar_wait(&k_full[k_st], k_ph, abort))) ok = false;
-          if (ok && pv && !(wait_v() && wait_p(it - 2))) ok = false;
+        continue;
+      }
+      if (tiles == 0) continue;  // no product, and no arrival on q_full
+      if (!wait(&q_full[team], queries++ & 1)) break;
+      tc_fence_after();
+      // Step i issues P V of tile i - 2, then Q K of tile i into the scores that P overlaid. Of the waits only the one
+      // for P is not long over, so it comes last; s_full is committed first: from a tile's P to the scores two tiles
+      // on and their softmax is the loop that sets the pace.
+      const int first = it, end = first + tiles;
+      for (; it < end + 2; ++it) {
+        const bool qk = it < end, pv = it - 2 >= first;
+        // the three tests go out together
+        const uint32_t k_ok = qk ? mbar_try_wait(&k_full[k_st], k_ph) : 1, v_ok = pv ? mbar_try_wait(&v_full[v_st], v_ph) : 1;
+        const uint32_t p_ok = pv ? mbar_try_wait(&p_full[team][it & 1], ((it - 2) >> 1) & 1) : 1;
+        if (!__all_sync(0xffffffffu, k_ok & v_ok & p_ok)) {
+          if (qk && !wait(&k_full[k_st], k_ph)) ok = false;
+          if (ok && pv && !(wait(&v_full[v_st], v_ph) && wait(&p_full[team][it & 1], ((it - 2) >> 1) & 1))) ok = false;
           if (!ok) break;
-          tc_fence_after();
-          if (leader) {
-            if (pv) issue_pv(it - 2);
-            if (qk) {
-              const uint64_t dk = dk0 + (uint64_t)(k_st * (KV_TILE_BYTES >> 4));
-              const uint32_t d_s = tmem + (it & 1) * KT;
-#pragma unroll
-              for (int kk = 0; kk < AD / 16; ++kk) {
-                const uint32_t qo = (kk >> 2) * Q_CHUNK + (kk & 3) * 32;
-                const uint32_t ko = (kk >> 2) * KV_CHUNK + (kk & 3) * 32;
-                tc_mma_bf16(d_s, dq0 + (uint64_t)(qo >> 4), dk + (uint64_t)(ko >> 4), IDESC_QK, kk > 0 ? 1u : 0u);
-              }
-              tc_commit(&s_full[it & 1]);
-              if constexpr (FEW) tc_commit(&k_empty[k_st]);
-            }
-            if (pv) commit_pv(it - 2);
-          }
-          __syncwarp();
-          issued = true;
-          if (qk) step(k_st, k_ph);
-          if (pv) step(v_st, v_ph);
         }
-        it = end;
+        tc_fence_after();
+        if (leader) {
+          const uint32_t d_s = tmem + (it & 1) * KT;  // the scores of tile it, and P of tile it - 2
+          if (pv) {
+            const uint64_t dv = dv0 + (uint64_t)(v_st * (KV_TILE_BYTES >> 4));
+#pragma unroll
+            for (int kk = 0; kk < KT / 16; ++kk)
+              tc_mma_bf16_ts(tmem + O_COL, d_s + kk * 8, dv + (uint64_t)(kk * 16 * 128 >> 4), IDESC_PV,
+                             (it - 2 > first || kk > 0) ? 1u : 0u);
+          }
+          if (qk) {
+            const uint64_t dk = dk0 + (uint64_t)(k_st * (KV_TILE_BYTES >> 4));
+#pragma unroll
+            for (int kk = 0; kk < AD / 16; ++kk) {
+              const uint32_t qo = (kk >> 2) * Q_CHUNK + (kk & 3) * 32;
+              const uint32_t ko = (kk >> 2) * KV_CHUNK + (kk & 3) * 32;
+              tc_mma_bf16(d_s, dq0 + (uint64_t)(qo >> 4), dk + (uint64_t)(ko >> 4), IDESC_QK, kk > 0 ? 1u : 0u);
+            }
+            tc_commit(&s_full[team][it & 1]);
+            tc_commit(&k_empty[k_st]);
+          }
+          if (pv) {
+            tc_commit(&pv_done[team][it & 1]);
+            tc_commit(&v_empty[v_st]);
+          }
+        }
+        __syncwarp();
+        issued = true;
+        if (qk) step(k_st, k_ph);
+        if (pv) step(v_st, v_ph);
       }
-      if (*abort && issued) {
-        if (leader) tc_commit(&drain_bar);
-        mbar_wait_drain(&drain_bar, 0);
-      }
+      it = end;
+    }
+    if (*abort && issued) {
+      if (leader) tc_commit(&drain_bar[team]);
+      mbar_wait_drain(&drain_bar[team], 0);
     }
     __syncwarp();
   } else {
     // ---- queries, softmax and output: warps w and w + 4 share TMEM lane quarter w & 3, 16 rows each;
     // threads t and t + 16 hold the same row and split its 64 scores and 128 output columns
-    const int quarter = warp & 3, sub = (warp - 2) >> 2, half = lane >> 4;
-    const int warp_row = quarter * 32 + sub * 16;
+    const int team = (warp - FIRST_SOFTMAX) >> 3;
+    const int quarter = warp & 3, sub = ((warp - FIRST_SOFTMAX) >> 2) & 1, half = lane >> 4;
+    const int team_row = quarter * 32 + sub * 16;                   // the warp's first row in its team's tile
+    const int warp_row = team * ROWS + team_row;                    // and among the item's rows
     const int row = warp_row + (lane & 15);
-    const uint32_t lane_off = (uint32_t)warp_row << 16;
+    const uint32_t lane_off = (uint32_t)team_row << 16;
+    const uint32_t tmem = tmem_base + team * TEAM_COLS;
+    uint8_t* q_smem = base + team * 2 * Q_CHUNK;
     const float sl2 = a.scale_log2;
     const long long qc = 2LL * (a.H + a.Hkv) * AD;
     constexpr int HK = KT / 2;
-    int it = 0, seg = 0, v_st = 0, v_ph = 0;
+    int it = 0, seg = 0;                 // the team's tiles, segments
+    int tile_no = 0, v_st = 0, v_ph = 0;  // the CTA's tiles, with the stage of V
     Segment s;
     // Segment's queries, normalised and rotated, into shared memory (row = token * G + head, 128-byte swizzle)
     auto next_segment = [&]() -> bool {
-      if (!__all_sync(0xffffffffu, mbar_wait(&seg_full[seg & 1], (seg >> 1) & 1, abort))) return false;
+      if (!warp_wait(&seg_full[seg & 1], (seg >> 1) & 1, abort)) return false;
       s = segs[seg & 1];
       if (s.n < 0) return false;
       // without tiles there is nothing to wait for on the other side, so q_full must not advance either: the
       // phase of a later segment could complete before the MMA thread has seen this one
-      if (s.tiles == 0) return true;
+      if (s.tiles == 0 || s.n * G <= team * ROWS) return true;
       const float4 w4 = *reinterpret_cast<const float4*>(a.qw + lane * 4);
       const int rows = min(16, s.n * G - warp_row);
 #pragma unroll 1
@@ -558,7 +603,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int rr = warp_row + min(i0 + i, rows - 1);
+          const int rr = warp_row + min(i0 + i, rows - 1) - team * ROWS;
           float v[4] = {bf16_lo(raw[i].x), bf16_hi(raw[i].x), bf16_lo(raw[i].y), bf16_hi(raw[i].y)};
           const float ss = warp_sum(v[0] * v[0] + v[1] * v[1] + v[2] * v[2] + v[3] * v[3]);
           const float rs = rsqrtf(ss / (float)AD + a.eps);
@@ -569,46 +614,47 @@ __global__ void __launch_bounds__(THREADS, 2)
           uint2 o;
           o.x = pack_bf16x2(v[0] * c[i].x - v[1] * sn[i].x, v[1] * c[i].x + v[0] * sn[i].x);
           o.y = pack_bf16x2(v[2] * c[i].y - v[3] * sn[i].y, v[3] * c[i].y + v[2] * sn[i].y);
-          *reinterpret_cast<uint2*>(base + (lane >> 4) * Q_CHUNK + rr * 128 + ((((lane & 15) >> 1) ^ (rr & 7)) << 4) +
+          *reinterpret_cast<uint2*>(q_smem + (lane >> 4) * Q_CHUNK + rr * 128 + ((((lane & 15) >> 1) ^ (rr & 7)) << 4) +
                                     (lane & 1) * 8) = o;
         }
       }
       fence_proxy_async_smem();
-      warp_arrive(&q_full, lane);
+      warp_arrive(&q_full[team], lane);
       return true;
     };
 
     bool ok = next_segment();
     while (ok) {
       const Segment cur = s;
-      const bool active = warp_row < cur.n * G;  // the warp holds rows of the segment
+      const bool active = warp_row < cur.n * G;            // the warp holds rows of the segment
+      const int tiles = cur.n * G > team * ROWS ? cur.tiles : 0;  // without rows the team computes none
       const int tok = row / G;
       int row_kend = cur.L;
       if (a.key_end && tok < cur.n) row_kend = min(max(a.key_end[cur.row0 + tok], cur.pos0 + tok + 1), cur.L);
       float m = -INFINITY, l = 0.f;
-      for (int i = 0; i < cur.tiles; ++i, ++it) {
+      for (int i = 0; i < tiles; ++i, ++it) {
         const int sb = it & 1, st = v_st, ph = v_ph;
         if (++v_st == STAGES) {
           v_st = 0;
           v_ph ^= 1;
         }
-        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[sb], (it >> 1) & 1, abort))) {
+        if (!warp_wait(&s_full[team][sb], (it >> 1) & 1, abort)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const int t0 = tile_of[it % TILE_RING] * KT;
+        const int tile = tile_of[(tile_no + i) % TILE_RING], t0 = tile & ~(KT - 1);
         const uint32_t sbase = tmem + lane_off + sb * KT;
         uint32_t vm0 = 0xffffffffu, vm1 = 0xffffffffu;
-        if ((a.text_mask && t0 < a.T) || t0 + KT > cur.L) {
+        if (tile & 1) {
           vm0 = __ballot_sync(0xffffffffu, key_used(a, cur.r, cur.L, t0 + lane));
           vm1 = __ballot_sync(0xffffffffu, key_used(a, cur.r, cur.L, t0 + 32 + lane));
           if ((vm0 & vm1) != 0xffffffffu) {  // the same for all warps: clear the V rows of unused keys
-            if (!__all_sync(0xffffffffu, mbar_wait(&v_full[st], ph, abort))) {
+            if (!warp_wait(&v_full[st], ph, abort)) {
               ok = false;
               break;
             }
-            const int key = (threadIdx.x - 64) >> 2, part = threadIdx.x & 3;
+            const int key = ((warp - FIRST_SOFTMAX) & 7) * 8 + (lane >> 2), part = lane & 3;
             const uint32_t vm = key < 32 ? vm0 : vm1;
             if (!((vm >> (key & 31)) & 1u)) {
               uint8_t* v = base + OFF_V + st * KV_TILE_BYTES + (part >> 1) * KV_CHUNK + key * 128 + (part & 1) * 64;
@@ -622,26 +668,26 @@ __global__ void __launch_bounds__(THREADS, 2)
           float v[HK];
           tmem_ld32_pair<HK>(sbase, v);
           const uint32_t vm = half ? vm1 : vm0;
-          if ((vm0 & vm1) != 0xffffffffu) {
+          if ((tile & 1) && (vm0 & vm1) != 0xffffffffu) {
 #pragma unroll
             for (int e = 0; e < HK; ++e)
               if (!((vm >> e) & 1u)) v[e] = -INFINITY;
           }
-          if (t0 + KT > cur.kmin) {
+          if (tile & 2) {
             const int lim = row_kend - (t0 + half * HK);
 #pragma unroll
             for (int e = 0; e < HK; ++e)
               if (e >= lim) v[e] = -INFINITY;
           }
-          float m4[4];
+          // the half row's maximum as a tree of three-input maxima
+          float m11[11], m4[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float x = v[k];
+          for (int k = 0; k < 10; ++k) m11[k] = fmax3(v[3 * k], v[3 * k + 1], v[3 * k + 2]);
+          m11[10] = fmaxf(v[30], v[31]);
 #pragma unroll
-            for (int t = 1; t < 7; t += 2) x = fmax3(x, v[k + 4 * t], v[k + 4 * t + 4]);
-            m4[k] = fmaxf(x, v[k + 28]);
-          }
-          const float hm = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          for (int k = 0; k < 3; ++k) m4[k] = fmax3(m11[3 * k], m11[3 * k + 1], m11[3 * k + 2]);
+          m4[3] = fmaxf(m11[9], m11[10]);
+          const float hm = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
           const float mx = fmaxf(hm, __shfl_xor_sync(0xffffffffu, hm, 16));
           const float mnew = fmaxf(m, mx * sl2);
           const bool grow = mnew > m + 8.0f;  // m = -inf on the first tile
@@ -656,7 +702,7 @@ __global__ void __launch_bounds__(THREADS, 2)
           l = l * alpha + rs;
           tmem_st16_pair<HK / 2>(sbase, pk);
           if (i >= 1 && any_grow) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, abort))) {
+            if (!warp_wait(&pv_done[team][(it - 1) & 1], ((it - 1) >> 1) & 1, abort)) {
               ok = false;
               break;
             }
@@ -674,9 +720,15 @@ __global__ void __launch_bounds__(THREADS, 2)
           tmem_wait_st();
         }
         tc_fence_before();
-        warp_arrive(&p_full[sb], lane);
+        warp_arrive(&p_full[team][sb], lane);
       }
       if (!ok) break;
+      tile_no += cur.tiles;
+      for (int i = tiles; i < cur.tiles; ++i)
+        if (++v_st == STAGES) {
+          v_st = 0;
+          v_ph ^= 1;
+        }
       // the last s_full was the last use of Q: the next segment's queries go in, and its first product
       // starts while this segment's output is written
       ++seg;
@@ -692,9 +744,9 @@ __global__ void __launch_bounds__(THREADS, 2)
       if (gated)
 #pragma unroll
         for (int q = 0; q < 4; ++q) gates[q] = __ldg(gp + q);
-      if (cur.tiles > 0) {
+      if (tiles > 0) {
         const int i = it - 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[i & 1], (i >> 1) & 1, abort))) break;
+        if (!warp_wait(&pv_done[team][i & 1], (i >> 1) & 1, abort)) break;
         tc_fence_after();
       }
       if (active) {
@@ -704,7 +756,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         for (int c = 0; c < AD / 64; ++c) {
           const int col = half * (AD / 2) + c * 32;
           float o[32];
-          if (cur.tiles > 0) {
+          if (tiles > 0) {
             tmem_ld32_pair<AD / 2>(tmem + lane_off + O_COL + c * 32, o);
           } else {
 #pragma unroll
@@ -747,15 +799,15 @@ __global__ void __launch_bounds__(THREADS, 2)
     if (place.r < a.b.R) {
       bool bad;
       const ItemPlan p = plan_of<QPOS>(a, place.r, &bad);
-      const int nth = (int)(place.offset / p.tiles), within = (int)(place.offset - (long long)nth * p.tiles);
-      // only the first place that cuts an item joins it
-      const long long start = (long long)blockIdx.x * place.share - within;
-      if (within > 0 && start >= ((long long)blockIdx.x - 1) * place.share) {
+      const int nth = (int)(place.offset / p.unit), at = (int)(place.offset - (long long)nth * p.unit);
+      // the first place that leaves tiles on both sides joins the item
+      const long long start = (long long)blockIdx.x * place.share - at;
+      if (at > SEGMENT_COST && at - place.share <= SEGMENT_COST) {
         const int item = p.rounds * a.ctas + nth, qt = item % p.qtiles;
         x.j = item / p.qtiles;
         x.rows = min(QPOS, p.q.n - qt * QPOS) * G;
         x.row0 = p.q.row0 + qt * QPOS;
-        x.last = (int)((start + p.tiles - 1) / place.share);
+        x.last = (int)((start + p.unit - 1) / place.share);
       }
     }
     a.joins[blockIdx.x] = x;
@@ -764,7 +816,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, TMEM_COLS);
+    tmem_dealloc(tmem_base, TEAMS * TEAM_COLS);
   }
 }
 
@@ -834,12 +886,13 @@ Shape shape_of(const Krea2PagedBatch& b, int H, int Hkv) {
   Shape s;
   // about one new token per request, or so few that an item of 16 rows holds them
   s.few = b.M <= 2LL * b.R || b.M * (long long)G <= 16;
-  const int rows = s.few ? 16 : 128, qpos = rows / G;
+  const int rows = s.few ? 16 : 128 * BIG_TEAMS, qpos = rows / G;
   const long long qtiles = b.M < b.M / qpos + b.R ? b.M : b.M / qpos + (long long)b.R;
   const long long tiles = ((long long)b.max_pages * b.page_size + KT - 1) / KT;
   s.split = tiles > MIN_SHARE;
   const long long most = qtiles * Hkv * (s.split ? (tiles + MIN_SHARE - 1) / MIN_SHARE : 1);
-  s.ctas = (int)(most < 2LL * num_sms() ? most : 2LL * num_sms());
+  const long long resident = (s.few || BIG_TEAMS == 1 ? 2LL : 1LL) * num_sms();
+  s.ctas = (int)(most < resident ? most : resident);
   if (s.ctas == 1) s.split = 0;
   s.part_rows = (long long)b.M * G < rows ? b.M * G : rows;
   s.o_bytes = s.split ? 2ull * s.ctas * s.part_rows * AD * 4 : 0;
@@ -879,7 +932,7 @@ int launch(const Krea2PagedBatch& b, const PagedAttnArgs& pa, const Shape& sh, v
   int rc;
   if ((rc = make_tmap_pages(&tk, pa.k_pages, pa.Hkv, b, a.group)) || (rc = make_tmap_pages(&tv, pa.v_pages, pa.Hkv, b, a.group)))
     return rc;
-  kern<<<sh.ctas, THREADS, SMEM_BYTES, stream>>>(tk, tv, a);
+  kern<<<sh.ctas, Cfg<G, FEW>::THREADS, SMEM_BYTES, stream>>>(tk, tv, a);
   count_launch();
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && sh.split) {
