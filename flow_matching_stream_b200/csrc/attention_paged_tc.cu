@@ -45,16 +45,13 @@ constexpr int KV_TILE_BYTES = 2 * KV_CHUNK;
 // FEW: batches of about one new token per request. With few rows a tile's time is that of its loads, and the room
 // of the other queries goes to K and V. (The MMA still reads 128 rows from each chunk of Q on, K's tiles behind the
 // 16; those accumulator rows are not used.)
-#ifndef BIG_TEAMS
-#define BIG_TEAMS 2
-#endif
 template <int G, bool FEW>
 struct Cfg {
-  static constexpr int TEAMS = FEW ? 1 : BIG_TEAMS;
+  static constexpr int TEAMS = FEW ? 1 : 2;
   static constexpr int ROWS = FEW ? 16 : 128;   // query rows of a team
   static constexpr int QPOS = TEAMS * ROWS / G;  // tokens of an item
-  static constexpr int STAGES = FEW ? 3 : TEAMS == 1 ? 2 : 5;
-  static constexpr int CTAS_PER_SM = TEAMS == 1 ? 2 : 1;
+  static constexpr int STAGES = FEW ? 3 : 5;
+  static constexpr int CTAS_PER_SM = FEW ? 2 : 1;
   static constexpr int FIRST_SOFTMAX = 1 + TEAMS;  // warp number
   static constexpr int THREADS = 32 * (1 + TEAMS + 8 * TEAMS);
   static constexpr int Q_CHUNK = ROWS * 128;    // ROWS x 64 bf16
@@ -67,7 +64,7 @@ constexpr uint32_t O_COL = 128;
 constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, KT, 0, 0);
 constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, AD, 0, 1);
 constexpr int MIN_SHARE = 4;         // key tiles: below that a CTA's start costs more than it shares
-constexpr int SEGMENT_COST = 4;      // what a segment's start and end cost, in tiles: items weigh that much more
+constexpr int SEGMENT_COST = 10;     // what a segment's start and end cost, in tiles: items weigh that much more
 constexpr int TILE_RING = 8;         // tile numbers in flight between warp 0 and the softmax warps
 
 struct Args {
@@ -213,12 +210,6 @@ __device__ __forceinline__ uint32_t used_tiles(const Args& a, int r, int L, int 
     for (int q = 0; q < 4; ++q) word |= (uint32_t)__any_sync(0xffffffffu, used[q]) << (i + q);
   }
   return word;
-}
-
-// The whole warp's wait; the usual case, a phase long complete, is one test and one vote.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
 }
 
 // One arrival per warp: 32 lanes' arrivals on one barrier are taken one after the other.
@@ -886,12 +877,12 @@ Shape shape_of(const Krea2PagedBatch& b, int H, int Hkv) {
   Shape s;
   // about one new token per request, or so few that an item of 16 rows holds them
   s.few = b.M <= 2LL * b.R || b.M * (long long)G <= 16;
-  const int rows = s.few ? 16 : 128 * BIG_TEAMS, qpos = rows / G;
+  const int rows = s.few ? 16 : 256, qpos = rows / G;
   const long long qtiles = b.M < b.M / qpos + b.R ? b.M : b.M / qpos + (long long)b.R;
   const long long tiles = ((long long)b.max_pages * b.page_size + KT - 1) / KT;
   s.split = tiles > MIN_SHARE;
   const long long most = qtiles * Hkv * (s.split ? (tiles + MIN_SHARE - 1) / MIN_SHARE : 1);
-  const long long resident = (s.few || BIG_TEAMS == 1 ? 2LL : 1LL) * num_sms();
+  const long long resident = (s.few ? 2LL : 1LL) * num_sms();
   s.ctas = (int)(most < resident ? most : resident);
   if (s.ctas == 1) s.split = 0;
   s.part_rows = (long long)b.M * G < rows ? b.M * G : rows;

@@ -253,7 +253,13 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
       if constexpr (LORA) lora_wait_prior_grid();
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    // LORA: the whole warp runs along, so that descriptors and counters are warp-uniform (they live in uniform registers,
+    // where the MMA takes them from), and one elected lane issues.
+    if (LORA || lane == 0) {
+      const bool leader = LORA ? elect_one() : true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return LORA ? warp_wait(bar, parity, abort) : mbar_wait(bar, parity, abort);
+      };
       uint32_t stage = 0, phase = 0;
       int local = 0;
       bool issued = false;
@@ -264,31 +270,38 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
       for (int t = blockIdx.x; t < total; t += gridDim.x, ++local) {
         const int acc = local & 1;
         const uint32_t acc_phase = (local >> 1) & 1;
-        if (!mbar_wait(&tempty_bar[acc], acc_phase ^ 1, abort)) break;
+        if (!wait(&tempty_bar[acc], acc_phase ^ 1)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BN;
         bool ok = true;
         int more = 0;
         for (int kb = 0; kb < nk; ++kb) {
-          if (!mbar_wait(&full_bar[stage], phase, abort)) {
+          if (!wait(&full_bar[stage], phase)) {
             ok = false;
             break;
           }
           tc_fence_after();
           uint64_t ad = da0 + (uint64_t)(stage * (stage_bytes >> 4));
           uint64_t bd = ad + (uint64_t)(w_off >> 4);
+          if (leader)
 #pragma unroll
-          for (int k = 0; k < BK / 16; ++k) tc_mma_bf16(d_tmem, ad + 2 * k, bd + 2 * k, Cfg::IDESC, (kb | k) != 0);
+            for (int k = 0; k < BK / 16; ++k) tc_mma_bf16(d_tmem, ad + 2 * k, bd + 2 * k, Cfg::IDESC, (kb | k) != 0);
           if constexpr (WIDE)
             for (int c = 1; c < kch; ++c) {
               ad += lt.a_pitch >> 4;
               bd += Cfg::B_BYTES >> 4;
+              if (leader)
 #pragma unroll
-              for (int k = 0; k < BK / 16; ++k) tc_mma_bf16(d_tmem, ad + 2 * k, bd + 2 * k, Cfg::IDESC, 1u);
+                for (int k = 0; k < BK / 16; ++k) tc_mma_bf16(d_tmem, ad + 2 * k, bd + 2 * k, Cfg::IDESC, 1u);
             }
           issued = true;
-          if (LORA && kb == nk - 1) more = *(volatile int*)&stage_more[stage];
-          tc_commit(&empty_bar[stage]);
+          if constexpr (LORA) {
+            if (kb == nk - 1) {
+              more = *(volatile int*)&stage_more[stage];
+              __syncwarp();  // all lanes have it before the stage is handed back
+            }
+          }
+          if (leader) tc_commit(&empty_bar[stage]);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
@@ -298,17 +311,19 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
           // columns of t: [high halves | low halves]; each meets the same columns of up
           const int steps = min(2 * lt.rankp / 16, 4), wrap = min(lt.rankp / 16, 4);
           while (ok && more) {
-            if (!mbar_wait(&full_bar[stage], phase, abort)) {
+            if (!wait(&full_bar[stage], phase)) {
               ok = false;
               break;
             }
             tc_fence_after();
             const uint64_t ad = da0 + (uint64_t)(stage * (stage_bytes >> 4));
             const uint64_t bd = ad + (uint64_t)(w_off >> 4);
-            for (int k = 0; k < steps; ++k)
-              tc_mma_bf16(d_tmem, ad + 2 * k, bd + 2 * (k >= wrap ? k - wrap : k), Cfg::IDESC, 1u);
+            if (leader)
+              for (int k = 0; k < steps; ++k)
+                tc_mma_bf16(d_tmem, ad + 2 * k, bd + 2 * (k >= wrap ? k - wrap : k), Cfg::IDESC, 1u);
             more = *(volatile int*)&stage_more[stage];
-            tc_commit(&empty_bar[stage]);
+            __syncwarp();
+            if (leader) tc_commit(&empty_bar[stage]);
             if (++stage == STAGES) {
               stage = 0;
               phase ^= 1;
@@ -316,11 +331,11 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
           }
         }
         if (!ok) break;
-        tc_commit(&tfull_bar[acc]);
+        if (leader) tc_commit(&tfull_bar[acc]);
       }
       if (*abort && issued) {
         // let every MMA already issued finish before TMEM is released
-        tc_commit(&drain_bar);
+        if (leader) tc_commit(&drain_bar);
         mbar_wait(&drain_bar, 0, &abort_flag /* already set: bounded by the timer below */);
         unsigned long long t0 = globaltimer_ns();
         while (!mbar_try_wait(&drain_bar, 0) && globaltimer_ns() - t0 < WAIT_LIMIT_NS) {

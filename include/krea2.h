@@ -458,6 +458,8 @@ int krea2_paged_kv_append(const Krea2Dims* dims, const Krea2PagedBatch* batch, i
  *     outputs zeros.
  * Keys past kv_len and keys that text_mask removes are not used, whatever their pages hold (NaN
  * included). A key that key_end hides from one token of a request but not from all must be finite.
+ * The same batch gives the same bits each time. Where long requests are cut and joined depends on the
+ * whole batch's lengths, so beside other requests a request's rows may round differently.
  *   workspace: krea2_paged_attention_workspace_size bytes, 256-byte aligned (NULL allowed when that
  *     is 0). It needs no initial value; calls that may overlap on the GPU need one each.
  * Kernels: bf16 with D = 128 and H/Hkv in {1, 2, 4} runs on the tensor cores; other shapes and fp32

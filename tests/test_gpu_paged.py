@@ -45,10 +45,10 @@ def run_attention(K2, b, text_mask=None, key_end=None, fill=7.0, ws=None):
     return out
 
 
-def compare(b, out, ref, size):
-    """Rows of requests against fp64, and zeros where a token has no readable key."""
-    used = b.start[-1]
-    out, ref, size = out[:used].double(), ref[:used], size[:used]
+def compare(b, out, ref, size, rows=None):
+    """Rows of requests (or `rows` of them) against fp64, and zeros where a token has no readable key."""
+    rows = slice(0, b.start[-1]) if rows is None else rows
+    out, ref, size = out[rows].double(), ref[rows], size[rows]
     rel, _ = off(out, ref)
     if b.dtype == torch.bfloat16:
         assert rel <= TOL_ATTN_BF16
@@ -288,7 +288,7 @@ def test_inconsistent_batches_are_reported_and_skipped(K2):
     # access inside the arrays, skip the request and report it
     d = dims(8, 2)
     good = Ragged(d, [3, 40, 2], [64, 200, 500], 16, torch.bfloat16, "cuda")
-    want = run_attention(K2, good)
+    ref, size = good.attention()
     for field, index, value in (("kv_len", 1, 39), ("kv_len", 1, 10 ** 6), ("kv_len", 1, -5), ("q_start", 1, 90),
                                 ("q_start", 2, -1), ("q_start", 3, 10 ** 6)):
         b = Ragged(d, [3, 40, 2], [64, 200, 500], 16, torch.bfloat16, "cuda")
@@ -303,7 +303,9 @@ def test_inconsistent_batches_are_reported_and_skipped(K2):
             K2.check_device_error()
         assert e.value.code == -1
         if field == "kv_len":  # the other requests are answered, the inconsistent one's rows stay
-            assert torch.equal(out[:3], want[:3]) and torch.equal(out[43:], want[43:])
+            # (not bit for bit: where long requests are cut depends on the whole batch's work)
+            compare(good, out, ref, size, slice(0, 3))
+            compare(good, out, ref, size, slice(43, 45))
             assert torch.all(out[3:43] == 7.0)
         K2.paged_kv_append(d, pb, b.qkvg, b.kw, b.cos, b.sin)
         with pytest.raises(K2.Krea2Error):
