@@ -194,7 +194,9 @@ __global__ void __launch_bounds__(DOWN_THREADS) lora_down_tc_kernel(const __grid
     }
     const __nv_bfloat16 high = __float2bfloat16_rn(v);
     dst[(size_t)row * (2 * rankp) + c] = high;
-    dst[(size_t)row * (2 * rankp) + rankp + c] = __float2bfloat16_rn(v - __bfloat162float(high));
+    // an infinite value has no low half (infinity minus itself would be NaN)
+    const float low = isinf(__bfloat162float(high)) ? 0.f : v - __bfloat162float(high);
+    dst[(size_t)row * (2 * rankp) + rankp + c] = __float2bfloat16_rn(low);
   }
   cluster_sync();  // no CTA ends while a peer still reads its part
   if (warp == 1) {

@@ -479,6 +479,9 @@ int krea2_gqa_attention_paged(const Krea2Dims* dims, const Krea2PagedBatch* batc
  *   up        (n_adapters, Nw, rank) in `dtype`, rows in the order of W's rows (for KREA2_EPI_SWIGLU
  *             gate and up rows interleaved in 64-row groups, for a fused projection stacked)
  *   rank      a multiple of 8, 8..256 (adapters of lower rank are padded with zeros)
+ * On the bf16 path the values of `up` must be finite: 128 rows share a tile, and a non-finite value of one
+ * request's adapter reaches the rows of the others in it. (Non-finite rows of A and of `down` stay with
+ * their own request.)
  * row_start that does not ascend from 0 to at most M, or an adapter number outside [-1, n_adapters),
  * sets the device error word (KREA2_ERR_ARG from krea2_check_device_error); the rows concerned are
  * then unspecified, and nothing outside the arrays is accessed. */

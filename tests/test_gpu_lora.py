@@ -106,6 +106,32 @@ def test_lora_without_adapters_is_linear(K2):
     assert rel <= 2 * TOL_BF16 and big <= 16 * TOL_BF16
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("epilogue", ["store", "swiglu", "resid"])
+def test_lora_empty_batch(K2, epilogue, dtype):
+    c = Case(K2, epilogue, [0, 0], 128, 256, 16, 2, dtype, spare=300)
+    assert torch.equal(c.run(), c.out0)
+    c.K2.check_device_error()
+
+
+def test_lora_many_requests(K2):
+    rows = [1 if r % 3 == 0 else (2 if r % 50 == 0 else 0) for r in range(900)]
+    Case(K2, "store", rows, 256, 256, 8, 5, torch.bfloat16, ids=[(r * 7) % 6 - 1 for r in range(900)], spare=3).check()
+
+
+def test_lora_infinite_low_rank_product(K2):
+    # down overflows for one request: its rows are infinite (or NaN where infinities cancel), others are not touched
+    c = Case(K2, "store", [10, 10], 128, 128, 8, 2, torch.bfloat16)
+    want = c.run()
+    c.A[10:] = 1.0
+    c.down[1] = 0.0
+    c.down[1, 0] = 3e38
+    c.up[1] = 1.0
+    got = c.run()
+    assert torch.equal(got[:10], want[:10])
+    assert torch.all(got[10:] == float("inf"))
+
+
 def test_lora_other_rows_do_not_matter(K2):
     # a row's result depends on its own values only: NaN in another request's rows of the same tile stays there
     c = Case(K2, "store", [20, 20, 20], 256, 256, 16, 3, torch.bfloat16)

@@ -162,6 +162,81 @@ def test_attention_masked_keys_may_hold_anything(K2):
         assert torch.equal(run_attention(K2, b, mask), want)
 
 
+@pytest.mark.parametrize("few", [False, True])
+def test_attention_key_ends_of_any_order(K2, few):
+    # values below a token's own position are raised to it, values past the last key cut to it, in any order
+    new, kv = ([1, 2, 1], [300, 700, 64]) if few else ([70, 3, 200], [300, 700, 220])
+    b = Ragged(dims(8, 2), new, kv, 16, torch.bfloat16, "cuda", spare=4)
+    g = torch.Generator().manual_seed(4)
+    end = torch.randint(-5, 900, (b.rows,), generator=g, dtype=torch.int32)
+    end[::7], end[3::7] = 0, 2 ** 31 - 1
+    check_attention(K2, b, key_end=end.cuda())
+    check_attention(K2, b, text_mask=random_mask(b, 250, 0.4), key_end=end.cuda())
+
+
+@pytest.mark.parametrize("new", [[1], [90]])
+def test_attention_long_sparse_masks(K2, new):
+    # more masked tiles than one word of the kernel's tile bits, and a mask longer than a request
+    b = Ragged(dims(8, 2), new + [2], [4000, 150], 64, torch.bfloat16, "cuda")
+    b.poison()
+    mask = torch.zeros(2, 3001, dtype=torch.uint8, device="cuda")
+    mask[0, [5, 1000, 1001, 2047, 2048, 2900]] = 1
+    mask[1, 70:149] = 1
+    check_attention(K2, b, text_mask=mask)
+    mask[0] = 0  # the first request sees only the keys behind the mask
+    check_attention(K2, b, text_mask=mask)
+
+
+@pytest.mark.parametrize("new", [[1, 1, 1], [100, 33, 3]])
+def test_attention_nan_token_stays_alone(K2, new):
+    b = Ragged(dims(8, 2), new, [400, 100, 300], 16, torch.bfloat16, "cuda")
+    want = run_attention(K2, b)
+    row = b.start[1]
+    b.qkvg[row, :b.d.HD] = float("nan")
+    got = run_attention(K2, b)
+    keep = torch.arange(b.rows, device="cuda") != row
+    assert torch.equal(got[keep], want[keep]) and torch.isnan(got[row]).all()
+
+
+@pytest.mark.parametrize("d,dtype", [(dims(8, 2), torch.bfloat16), (D64, torch.float32)])
+def test_empty_batches(K2, d, dtype):
+    # no request has a new token: nothing is written
+    b = Ragged(d, [0, 0, 0], [0, 70, 16], 16, dtype, "cuda", spare=40)
+    k0 = b.k_pages.clone()
+    K2.paged_kv_append(d, batch_of(K2, b), b.qkvg, b.kw, b.cos, b.sin)
+    out = run_attention(K2, b)
+    assert torch.all(out == 7.0) and torch.equal(b.k_pages, k0)
+
+
+def test_attention_many_requests(K2):
+    # more requests than a block has threads, most of them empty
+    n = [1 if r % 5 == 0 else (3 if r % 41 == 0 else 0) for r in range(1500)]
+    kv = [max(n[r], (r * 37) % 200) for r in range(1500)]
+    b = Ragged(dims(4, 1), n, kv, 16, torch.bfloat16, "cuda", spare=2)
+    b.poison()
+    K2.paged_kv_append(b.d, batch_of(K2, b), b.qkvg, b.kw, b.cos, b.sin)
+    check_attention(K2, b)
+
+
+@pytest.mark.parametrize("d,dtype,page", [(dims(8, 2), torch.bfloat16, 64), (D64, torch.float32, 16)])
+def test_offsets_past_32_bits(K2, d, dtype, page):
+    # a pool of more than 2^31 elements; the requests' pages lie at its end
+    b = Ragged(d, [1, 40], [200, 130], page, dtype, "cuda")
+    pages = 2 ** 31 // (page * d.KVD) + b.num_pages + 1
+    kp, vp = (torch.empty(pages, page, d.KVD, device="cuda", dtype=dtype) for _ in range(2))
+    first = pages - b.num_pages
+    kp[first:], vp[first:] = b.k_pages, b.v_pages
+    b.table = torch.where(b.table >= 0, b.table + first, b.table)
+    b.k_pages, b.v_pages, b.num_pages = kp, vp, pages
+    pb = batch_of(K2, b)
+    K2.paged_kv_append(d, pb, b.qkvg, b.kw, b.cos, b.sin)
+    check_attention(K2, b)
+    for r in range(b.R):
+        p, s = b.slots(r)
+        want = b.qkvg[b.rowsof(r), d.HD + d.KVD:d.HD + 2 * d.KVD]
+        assert torch.equal(vp[p[-b.new[r]:], s[-b.new[r]:]], want)
+
+
 def test_attention_shared_prefix_pages(K2):
     # two requests whose first pages are the same ones
     b = Ragged(dims(8, 2), [3, 9], [140, 150], 16, torch.bfloat16, "cuda")
