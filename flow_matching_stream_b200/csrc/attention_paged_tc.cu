@@ -26,6 +26,8 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <type_traits>
+
 #include "attention_device.cuh"
 #include "krea2_device.cuh"
 #include "krea2_internal.h"
@@ -614,10 +616,92 @@ __global__ void __launch_bounds__(Cfg<G, FEW>::THREADS, Cfg<G, FEW>::CTAS_PER_SM
       return true;
     };
 
+    // One tile of scores to P. Tiles with masked keys, with row limits inside them or with V rows to clear take a form of
+    // their own: with its tests in the common one, that took 8 % longer.
+    bool active = false;  // the warp holds rows of the segment
+    auto softmax_tile = [&](auto partial, int tile, int i, int n, int st, int ph, const Segment& cur, int row_kend,
+                            float& m, float& l) -> bool {
+      constexpr bool PARTIAL = decltype(partial)::value;
+      const int sb = n & 1, t0 = tile & ~(KT - 1);
+      uint32_t vm0 = 0xffffffffu, vm1 = 0xffffffffu;
+      const uint32_t sbase = tmem + lane_off + sb * KT;
+      if constexpr (PARTIAL) {
+        if (tile & 1) {
+          vm0 = __ballot_sync(0xffffffffu, key_used(a, cur.r, cur.L, t0 + lane));
+          vm1 = __ballot_sync(0xffffffffu, key_used(a, cur.r, cur.L, t0 + 32 + lane));
+          if ((vm0 & vm1) != 0xffffffffu) {  // the same for all warps: clear the V rows of unused keys
+            if (!warp_wait(&v_full[st], ph, abort)) return false;
+            const int key = ((warp - FIRST_SOFTMAX) & 7) * 8 + (lane >> 2), part = lane & 3;
+            const uint32_t vm = key < 32 ? vm0 : vm1;
+            if (!((vm >> (key & 31)) & 1u)) {
+              uint8_t* v = base + OFF_V + st * KV_TILE_BYTES + (part >> 1) * KV_CHUNK + key * 128 + (part & 1) * 64;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) reinterpret_cast<uint4*>(v)[q] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+          }
+        }
+      }
+      if (PARTIAL && !active) return true;
+      float v[HK];
+      tmem_ld32_pair<HK>(sbase, v);
+      if constexpr (PARTIAL) {
+        const uint32_t vm = half ? vm1 : vm0;
+        if ((tile & 1) && (vm0 & vm1) != 0xffffffffu) {
+#pragma unroll
+          for (int e = 0; e < HK; ++e)
+            if (!((vm >> e) & 1u)) v[e] = -INFINITY;
+        }
+        if (tile & 2) {
+          const int lim = row_kend - (t0 + half * HK);
+#pragma unroll
+          for (int e = 0; e < HK; ++e)
+            if (e >= lim) v[e] = -INFINITY;
+        }
+      }
+      // the half row's maximum as a tree of three-input maxima
+      float m11[11], m4[4];
+#pragma unroll
+      for (int k = 0; k < 10; ++k) m11[k] = fmax3(v[3 * k], v[3 * k + 1], v[3 * k + 2]);
+      m11[10] = fmaxf(v[30], v[31]);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) m4[k] = fmax3(m11[3 * k], m11[3 * k + 1], m11[3 * k + 2]);
+      m4[3] = fmaxf(m11[9], m11[10]);
+      const float hm = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
+      const float mx = fmaxf(hm, __shfl_xor_sync(0xffffffffu, hm, 16));
+      const float mnew = fmaxf(m, mx * sl2);
+      const bool grow = mnew > m + 8.0f;  // m = -inf on the first tile
+      float alpha = 1.f;
+      const bool any_grow = __any_sync(0xffffffffu, grow);
+      if (grow) {
+        alpha = ex2(m - mnew);  // 0 on the first tile
+        m = mnew;
+      }
+      uint32_t pk[HK / 2];
+      const float rs = exp_tile<HK>(v, sl2, m == -INFINITY ? 0.f : m, pk);
+      l = l * alpha + rs;
+      tmem_st16_pair<HK / 2>(sbase, pk);
+      if (i >= 1 && any_grow) {
+        if (!warp_wait(&pv_done[team][(n - 1) & 1], ((n - 1) >> 1) & 1, abort)) return false;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < AD / 64; ++c) {
+          float o[32];
+          const uint32_t oa = tmem + lane_off + O_COL + c * 32;
+          tmem_ld32_pair<AD / 2>(oa, o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] *= alpha;
+          tmem_st32_pair<AD / 2>(oa, o);
+        }
+      }
+      tmem_wait_st();
+      return true;
+    };
+
     bool ok = next_segment();
     while (ok) {
       const Segment cur = s;
-      const bool active = warp_row < cur.n * G;            // the warp holds rows of the segment
+      active = warp_row < cur.n * G;
       const int tiles = cur.n * G > team * ROWS ? cur.tiles : 0;  // without rows the team computes none
       const int tok = row / G;
       int row_kend = cur.L;
@@ -634,82 +718,13 @@ __global__ void __launch_bounds__(Cfg<G, FEW>::THREADS, Cfg<G, FEW>::CTAS_PER_SM
           break;
         }
         tc_fence_after();
-        const int tile = tile_of[(tile_no + i) % TILE_RING], t0 = tile & ~(KT - 1);
-        const uint32_t sbase = tmem + lane_off + sb * KT;
-        uint32_t vm0 = 0xffffffffu, vm1 = 0xffffffffu;
-        if (tile & 1) {
-          vm0 = __ballot_sync(0xffffffffu, key_used(a, cur.r, cur.L, t0 + lane));
-          vm1 = __ballot_sync(0xffffffffu, key_used(a, cur.r, cur.L, t0 + 32 + lane));
-          if ((vm0 & vm1) != 0xffffffffu) {  // the same for all warps: clear the V rows of unused keys
-            if (!warp_wait(&v_full[st], ph, abort)) {
-              ok = false;
-              break;
-            }
-            const int key = ((warp - FIRST_SOFTMAX) & 7) * 8 + (lane >> 2), part = lane & 3;
-            const uint32_t vm = key < 32 ? vm0 : vm1;
-            if (!((vm >> (key & 31)) & 1u)) {
-              uint8_t* v = base + OFF_V + st * KV_TILE_BYTES + (part >> 1) * KV_CHUNK + key * 128 + (part & 1) * 64;
-#pragma unroll
-              for (int q = 0; q < 4; ++q) reinterpret_cast<uint4*>(v)[q] = make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
-          }
+        const int tile = tile_of[(tile_no + i) % TILE_RING];
+        if ((tile & 3) == 0) {
+          if (active) ok = softmax_tile(std::false_type(), tile, i, it, st, ph, cur, row_kend, m, l);
+        } else {
+          ok = softmax_tile(std::true_type(), tile, i, it, st, ph, cur, row_kend, m, l);
         }
-        if (active) {
-          float v[HK];
-          tmem_ld32_pair<HK>(sbase, v);
-          const uint32_t vm = half ? vm1 : vm0;
-          if ((tile & 1) && (vm0 & vm1) != 0xffffffffu) {
-#pragma unroll
-            for (int e = 0; e < HK; ++e)
-              if (!((vm >> e) & 1u)) v[e] = -INFINITY;
-          }
-          if (tile & 2) {
-            const int lim = row_kend - (t0 + half * HK);
-#pragma unroll
-            for (int e = 0; e < HK; ++e)
-              if (e >= lim) v[e] = -INFINITY;
-          }
-          // the half row's maximum as a tree of three-input maxima
-          float m11[11], m4[4];
-#pragma unroll
-          for (int k = 0; k < 10; ++k) m11[k] = fmax3(v[3 * k], v[3 * k + 1], v[3 * k + 2]);
-          m11[10] = fmaxf(v[30], v[31]);
-#pragma unroll
-          for (int k = 0; k < 3; ++k) m4[k] = fmax3(m11[3 * k], m11[3 * k + 1], m11[3 * k + 2]);
-          m4[3] = fmaxf(m11[9], m11[10]);
-          const float hm = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
-          const float mx = fmaxf(hm, __shfl_xor_sync(0xffffffffu, hm, 16));
-          const float mnew = fmaxf(m, mx * sl2);
-          const bool grow = mnew > m + 8.0f;  // m = -inf on the first tile
-          float alpha = 1.f;
-          const bool any_grow = __any_sync(0xffffffffu, grow);
-          if (grow) {
-            alpha = ex2(m - mnew);  // 0 on the first tile
-            m = mnew;
-          }
-          uint32_t pk[HK / 2];
-          const float rs = exp_tile<HK>(v, sl2, m == -INFINITY ? 0.f : m, pk);
-          l = l * alpha + rs;
-          tmem_st16_pair<HK / 2>(sbase, pk);
-          if (i >= 1 && any_grow) {
-            if (!warp_wait(&pv_done[team][(it - 1) & 1], ((it - 1) >> 1) & 1, abort)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < AD / 64; ++c) {
-              float o[32];
-              const uint32_t oa = tmem + lane_off + O_COL + c * 32;
-              tmem_ld32_pair<AD / 2>(oa, o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] *= alpha;
-              tmem_st32_pair<AD / 2>(oa, o);
-            }
-          }
-          tmem_wait_st();
-        }
+        if (!ok) break;
         tc_fence_before();
         warp_arrive(&p_full[team][sb], lane);
       }
