@@ -826,9 +826,9 @@ __global__ void __launch_bounds__(Cfg<G, FEW>::THREADS, Cfg<G, FEW>::CTAS_PER_SM
   }
 }
 
-constexpr int JOIN_ROWS = 16;
+constexpr int JOIN_ROWS = 8;  // one per warp
 
-// Joins the parts of cut items: block (c, y), for 16 rows, looks at the place where CTA c's share starts, and
+// Joins the parts of cut items: block (c, y), for eight rows, looks at the place where CTA c's share starts, and
 // joins the item that is cut there if no earlier place cuts it. Parts come in key order, so results repeat bit
 // for bit. Launched as a programmatic dependent of the kernel above.
 template <int G>
@@ -843,19 +843,33 @@ __global__ void __launch_bounds__(256) paged_attn_join_kernel(Args a) {
     const long long prow = x.row0 + row / G;
     const uint2 g = *reinterpret_cast<const uint2*>(a.qkvg + prow * qc + (a.H + 2 * a.Hkv + h) * AD + lane * 4);
     const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + row;
-    auto slot_of = [&](int k) { return (long long)(k < c ? 2 * (c - 1) + 1 : 2 * k) * a.part_rows; };
+    const float4* po = reinterpret_cast<const float4*>(a.part_o + (long long)row * AD) + lane;
+    auto slot_of = [&](int k) { return (long long)(k == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + k)) * a.part_rows; };
     float o[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f, top = -INFINITY;
-    for (int k = c - 1; k <= x.last; ++k) {
-      const float2 v = ml[slot_of(k)];
-      const float4 y = *reinterpret_cast<const float4*>(a.part_o + (slot_of(k) + row) * AD + lane * 4);
-      if (v.x == -INFINITY && v.y == 0.f) continue;  // no readable key in this part
-      const float m = fmaxf(top, v.x);
-      const float old = top == -INFINITY ? 0.f : ex2(top - m), w = ex2(v.x - m);
-      sum = sum * old + w * v.y;
-      o[0] = o[0] * old + w * y.x;
-      o[1] = o[1] * old + w * y.y;
-      o[2] = o[2] * old + w * y.z;
-      o[3] = o[3] * old + w * y.w;
+    // 32 parts at a time: a lane takes a part's maximum and sum, then the warp takes the parts' rows, four in flight
+    const int parts = x.last - c + 2;
+    for (int k0 = 0; k0 < parts; k0 += 32) {
+      float2 v = make_float2(-INFINITY, 0.f);
+      if (k0 + lane < parts) v = ml[slot_of(k0 + lane)];
+      float m = fmaxf(top, v.x);
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+      const float old = top == -INFINITY ? 0.f : ex2(top - m);
+      // a part without a readable key counts nothing
+      const float w = v.x == -INFINITY && v.y == 0.f ? 0.f : ex2(v.x - m);
+      sum = sum * old + warp_sum(w * v.y);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] *= old;
+      const int n = min(32, parts - k0);
+#pragma unroll 4
+      for (int k = 0; k < n; ++k) {
+        const float4 y = po[slot_of(k0 + k) * (AD / 4)];
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+        o[0] += wk * y.x;
+        o[1] += wk * y.y;
+        o[2] += wk * y.z;
+        o[3] += wk * y.w;
+      }
       top = m;
     }
     const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
