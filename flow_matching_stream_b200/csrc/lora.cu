@@ -36,6 +36,8 @@ __device__ __forceinline__ int adapter_of_row(const Krea2Lora& l, int row) {
 __global__ void __launch_bounds__(256) lora_down_simt_kernel(Krea2Lora l, int M, int K, const float* __restrict__ A,
                                                              float* __restrict__ t) {
   check_lora(l, M);
+  // the projection behind this grid may start (it waits for t itself)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const long gw = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   const int row = (int)(gw / l.rank), j = (int)(gw % l.rank);
@@ -67,7 +69,10 @@ __global__ void __launch_bounds__((TM / RM) * (TN / (2 * HC)))
   const int m0 = blockIdx.y * TM, c0 = (blockIdx.x / PER_GROUP) * 128 + (blockIdx.x % PER_GROUP) * HALF;
   auto col = [&](int c) { return c0 + (c % HALF) + (c / HALF) * 64; };  // of the tile's column c
   const int used = used_rows(l, M);
-  if (m0 >= used) return;
+  if (m0 >= used) {
+    lora_wait_prior_grid();
+    return;
+  }
   float acc[RM][2 * HC];
 #pragma unroll
   for (int i = 0; i < RM; ++i)
@@ -111,6 +116,7 @@ __global__ void __launch_bounds__((TM / RM) * (TN / (2 * HC)))
     }
     __syncthreads();
   }
+  lora_wait_prior_grid();  // t is written by the grid before this one
 #pragma unroll
   for (int i = 0; i < RM; ++i) {
     const int r = m0 + ty * RM + i;
@@ -173,13 +179,20 @@ int lora_simt(int epi, const LoraLinearArgs& a, const Krea2Lora& l, float* t, cu
   const bool small = (long long)groups * ((a.M + 63) / 64) < 2L * num_sms();
   const dim3 grid(small ? groups * 4 : groups, small ? (a.M + 15) / 16 : (a.M + 63) / 64);
   if (grid.y > 65535) return set_error(KREA2_ERR_UNSUPPORTED, "more than %d rows", 65535 * 64);
-#define KREA2_LORA(E)                                                                                            \
-  if (small)                                                                                                     \
-    lora_linear_simt_kernel<16, 32, 1, 2, 64, E><<<grid, 128, 0, stream>>>(l, a.M, a.N, a.K, A, W, t, a.out, a.gate, \
-                                                                          a.rows_per_batch, a.gate_stride);      \
-  else                                                                                                           \
-    lora_linear_simt_kernel<64, 128, 4, 4, 16, E><<<grid, 256, 0, stream>>>(l, a.M, a.N, a.K, A, W, t, a.out, a.gate, \
-                                                                           a.rows_per_batch, a.gate_stride)
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(small ? 128 : 256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaError_t e;
+#define KREA2_LORA(E)                                                                                              \
+  e = cudaLaunchKernelEx(&cfg, small ? lora_linear_simt_kernel<16, 32, 1, 2, 64, E>                                \
+                                     : lora_linear_simt_kernel<64, 128, 4, 4, 16, E>,                              \
+                         l, a.M, a.N, a.K, A, W, (const float*)t, a.out, a.gate, a.rows_per_batch, a.gate_stride)
   if (epi == EPI_STORE) {
     KREA2_LORA(EPI_STORE);
   } else if (epi == EPI_SWIGLU) {
@@ -188,7 +201,9 @@ int lora_simt(int epi, const LoraLinearArgs& a, const Krea2Lora& l, float* t, cu
     KREA2_LORA(EPI_RESID);
   }
 #undef KREA2_LORA
-  return check_launch("lora_linear");
+  count_launch();
+  if (e != cudaSuccess) return set_error(KREA2_ERR_CUDA, "lora_linear launch failed: %s", cudaGetErrorString(e));
+  return KREA2_OK;
 }
 
 }  // namespace
