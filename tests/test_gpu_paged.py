@@ -133,6 +133,24 @@ def test_attention_full_heads_long(K2):
     check_attention(K2, b, text_mask=random_mask(b, 512, 0.3))
 
 
+def test_attention_whole_rounds(K2):
+    # more items (64 tokens of a KV head) than CTAs: whole items in turn, the rest in equal shares
+    b = Ragged(KI.FULL, [900, 70], [1000, 300], 64, torch.bfloat16, "cuda")
+    b.poison()
+    check_attention(K2, b)
+    check_attention(K2, b, key_end=causal(b))
+
+
+def test_attention_short_tables_are_not_cut(K2):
+    # tables of at most 256 keys: items are handed out whole
+    b = Ragged(dims(8, 2), [190] * 38 + [1, 0, 77], [190] * 38 + [192, 3, 77], 64, torch.bfloat16, "cuda", spare=2)
+    b.poison()
+    check_attention(K2, b, key_end=causal(b))
+    few = Ragged(dims(8, 2), [1] * 90, [1 + (7 * r) % 180 for r in range(90)], 64, torch.bfloat16, "cuda")
+    few.poison()
+    check_attention(K2, few)
+
+
 @pytest.mark.parametrize("keep", [0.0, 0.02, 0.9])
 def test_attention_masks(K2, keep):
     # keep 0: requests shorter than the mask have no readable key at all and output zeros
