@@ -93,7 +93,7 @@ _GEMM_SOURCES = ("gemm_tcgen05.cu", "krea2_device.cuh", "krea2_internal.h")
 KERNEL_SOURCES = {
     "qkv_proj": _GEMM_SOURCES, "out_proj_resid": _GEMM_SOURCES, "gate_up_swiglu": _GEMM_SOURCES,
     "down_proj_resid": _GEMM_SOURCES,
-    "attention": ("attention_tc.cu", "krea2_device.cuh", "krea2_internal.h"),
+    "attention": ("attention_tc.cu", "attention_device.cuh", "krea2_device.cuh", "krea2_internal.h"),
 }
 
 

@@ -703,7 +703,9 @@ int launch_gemm_bn(const GemmParams& p0, const void* A, const void* W, cudaStrea
 }
 
 // The GEMM with the adapters' K steps, launched as a programmatic dependent of lora_down: its CTAs
-// start as soon as every lora_down CTA runs, and wait for t only when they first load it.
+// start as soon as every lora_down CTA runs, and wait for t only when they first load it. Bound by the tensor
+// cores, under the power cap: gate/up of 5760 rows, rank 16, 1.82 ms with t's own kernel (1280 TFLOP/s, 93 % of
+// the sustained matrix rate). The shared projection alone takes 1.74 to 1.81 ms from run to run.
 template <int BN, int EPI, bool WIDE>
 int launch_gemm_lora_bn(const GemmParams& p0, const void* A, const void* W, const Krea2Lora& l, const void* t,
                         cudaStream_t stream) {
@@ -731,10 +733,12 @@ int launch_gemm_lora_bn(const GemmParams& p0, const void* A, const void* W, cons
     if (p.M < BM) a_rows = (p.M + 7) / 8 * 8;
     lt.a_pitch = a_rows * BK * 2;
     // One row tile streams W once, and a stage's turn (a wait, a load of A and one of W by one thread) takes
-    // about 0.3 us whatever it loads: as many K steps a stage as leave three stages. 6144 x 6144 by one row:
-    // 34 us with one K step a stage, 17 us with four.
+    // about 0.3 us whatever it loads: as many K steps a stage as leave three stages. One row by 6144 x 6144 with an
+    // adapter: 30.9 us with one K step a stage (30.8 us for N = 1024 too), 22.9 with two, 21.2 with four. What is
+    // left is W's 128-byte operand columns: loads alone in that order reach 3.8 TB/s from HBM, in runs of 512 bytes
+    // a row, which the operand layout does not allow, 5.2 TB/s. A ring holds two steps of 128 rows at least.
     const int step = lt.a_pitch + Cfg::B_BYTES, ring = Cfg::STAGES * Cfg::STAGE_BYTES;
-    lt.kch = 12 * step <= ring ? 4 : 6 * step <= ring ? 2 : 1;
+    lt.kch = 12 * step <= ring ? 4 : 2;
     lt.stage_bytes = lt.kch * step;
     lt.stages = ring / lt.stage_bytes;
     if (lt.stages > MAX_STAGES) lt.stages = MAX_STAGES;
@@ -812,7 +816,8 @@ int gemm_bf16_lora(int epi, const GemmParams& p, const void* A, const void* W, c
   const long tm = (p.M + BM - 1) / BM;
   const double e128 = wave_eff(tm * (p.N / 128), sms);
   if (tm == 1) {
-    // few tiles: narrower ones put more SMs on the stream of W (a SwiGLU tile is 128 columns at least)
+    // few tiles: narrower ones put more SMs on the stream of W (a SwiGLU tile is 128 columns at least). One row
+    // by 6144 x 6144: 21.2 us in 64 columns, 24.8 in 128; x 15360, where both fill the SMs: 38.0 and 36.5.
     const bool narrow = wave_eff(p.N / 64, sms) > 1.25 * e128;
     if (epi == EPI_SWIGLU) return launch_gemm_lora_bn<128, EPI_SWIGLU, true>(p, A, W, l, t, stream);
     if (epi == EPI_STORE)

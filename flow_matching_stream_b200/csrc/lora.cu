@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(256) lora_down_simt_kernel(Krea2Lora l, int M,
   if (id >= 0) {
     const float* x = A + (long)row * K;
     const float* d = reinterpret_cast<const float*>(l.down) + ((long)id * l.rank + j) * K;
-    for (int k = lane; k < K; k += 32) s += (x[k]) * (d[k]);
+    for (int k = lane; k < K; k += 32) s += x[k] * d[k];
     s = warp_sum(s) * l.scale[id];
   }
   if (lane == 0) t[(long)row * l.rank + j] = s;

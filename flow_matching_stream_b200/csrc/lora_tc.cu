@@ -4,7 +4,10 @@
 // Bound by reading A (and down) once: 2 M K r operations on 2 M K bytes are 16 operations a byte at
 // rank 16. One cluster per unit; its CTAs split K, each accumulates its part in TMEM (tcgen05, M = 128,
 // N = rank), puts the fp32 part into its own shared memory, and sums a slice of the rows over all parts
-// through distributed shared memory in a fixed order, so that results repeat bit for bit.
+// through distributed shared memory in a fixed order, so that results repeat bit for bit. t is kept to 16 bits
+// of mantissa as two halves: rounded to bf16 once, it would be the largest error of an fp32 residual, and the
+// second half costs the GEMM one more K step of 16 to 64 per 6144 or more. Measured: 16 us for 1589 x 6144,
+// rank 64; 38 us for 4818 x 16384, rank 32 (4.1 TB/s).
 #include <cuda.h>
 
 #include "krea2_device.cuh"

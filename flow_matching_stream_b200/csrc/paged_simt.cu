@@ -70,6 +70,7 @@ struct alignas(sizeof(T) * E) Pack {
 
 // One warp per (row, four KV heads), bound by its bytes: k and v of the four heads are on their way (8 or 16 bytes a
 // lane) while the row's request and page are looked up. Each lane holds D / 32 columns (whole rotation pairs).
+// 8192 tokens of 12 heads: 20.6 us, 5.1 TB/s (78 % of a copy's rate); with one head a warp it took 38.9 us.
 constexpr int APPEND_HEADS = 4;
 template <typename T, int D>
 __global__ void __launch_bounds__(256) paged_append_kernel(PagedArgs p, const T* __restrict__ qkvg, int H, int Hkv,
