@@ -4,9 +4,9 @@
 //
 // Bound: the tensor cores and the exponentials for many new tokens (4 D H operations a token and key),
 // reading K and V once (512 bytes a key and KV head) for few. Measured (48 q / 12 kv heads, pages of 64): two
-// requests of 4096 new tokens over 8704 keys 1.71 ms, 1020 TFLOP/s under the power cap (74 % of the sustained matrix
-// rate), with tensor pipe, exponentials and issue slots each about half busy (smaller batch: 48, 52 and 53 %); eight
-// single tokens over 521 to 8704 keys 51 us, 4.5 TB/s, of which the join alone is 7.
+// requests of 4096 new tokens over 8704 keys 1.69 to 1.80 ms by box, 970 to 1040 TFLOP/s under the power cap (71 to
+// 75 % of the sustained matrix rate), with tensor pipe, exponentials and issue slots each about half busy (a smaller
+// batch: 48, 52 and 53 %); eight single tokens over 521 to 8704 keys 50 to 53 us, 4.3 to 4.6 TB/s, the join 7 of them.
 //
 // Roundings: q_hat and P go to the tensor cores in bf16, as K and V come; maxima, sums and O are fp32. Against fp64
 // the output is off by 0.0025 to 0.0029 of its size, where its own rounding to bf16 makes 0.0017. Carrying what those

@@ -704,7 +704,7 @@ int launch_gemm_bn(const GemmParams& p0, const void* A, const void* W, cudaStrea
 
 // The GEMM with the adapters' K steps, launched as a programmatic dependent of lora_down: its CTAs
 // start as soon as every lora_down CTA runs, and wait for t only when they first load it. Bound by the tensor
-// cores, under the power cap: gate/up of 5760 rows, rank 16, 1.82 ms with t's own kernel (1280 TFLOP/s, 93 % of
+// cores, under the power cap: gate/up of 5760 rows, rank 16, 1.82 to 1.87 ms by box with t's own kernel (90 to 93 % of
 // the sustained matrix rate). The shared projection alone takes 1.74 to 1.81 ms from run to run.
 template <int BN, int EPI, bool WIDE>
 int launch_gemm_lora_bn(const GemmParams& p0, const void* A, const void* W, const Krea2Lora& l, const void* t,
