@@ -328,6 +328,13 @@ def backbone_forward(dims, B: int, T: int, N: int, hidden_states: torch.Tensor, 
 # These calls are short next to what a checked argument costs in Python, so each tensor is checked by one
 # function that looks at nothing twice and words its complaint only when there is one.
 
+def _int32(v: int, name: str) -> int:
+    # ctypes would pass on the low 32 bits of a larger number
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{name} = {v} does not fit 32 bits")
+    return v
+
+
 def _complain(t: Optional[torch.Tensor], dev: int, dtype: torch.dtype, shape: tuple, name: str) -> None:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
@@ -533,6 +540,7 @@ def lora_linear(epilogue: int, A: torch.Tensor, W: torch.Tensor, adapters: LoraA
             raise ValueError("a residual epilogue needs a gate")
         if gate_stride is None:
             gate_stride = gate.shape[-1]
+        _int32(rows_per_batch, "rows_per_batch")
         rows = R if rows_per_batch == 0 else (M + rows_per_batch - 1) // max(rows_per_batch, 1)
         if gate.numel() < (rows - 1) * gate_stride + Nw:
             raise ValueError(f"the gate has {gate.numel()} values, {rows} rows of stride {gate_stride} are read")

@@ -132,3 +132,17 @@ def test_binding_checks_tensors(K2):
         K2.LoraAdapters(t(2, 16, 64), t(2, 128, 8), t(2))
     with pytest.raises(TypeError):
         K2.LoraAdapters(t(2, 16, 64), t(2, 128, 16), t(2, dtype=torch.float64))
+
+
+def test_rows_per_batch_that_does_not_fit_32_bits(K2):
+    # its low 32 bits are 0, which would read a gate row per request where the caller's gate has one row
+    import types
+
+    from flow_matching_stream_b200 import _lib
+    t, bf = torch.zeros, torch.bfloat16
+    adapters = types.SimpleNamespace(dev=0, dtype=bf, K=64, Nw=128, rank=16, struct=_lib.Krea2Lora())
+    for rows_per_batch in (2 ** 32, 2 ** 31, -2 ** 31 - 1):
+        with pytest.raises(ValueError, match="rows_per_batch"):
+            K2.lora_linear(K2.KREA2_EPI_RESID, t(10, 64, dtype=bf), t(128, 64, dtype=bf), adapters,
+                           t(4, dtype=torch.int32), t(3, dtype=torch.int32), t(10, 128), t(1 << 16, dtype=torch.uint8),
+                           gate=t(1, 128), rows_per_batch=rows_per_batch)
