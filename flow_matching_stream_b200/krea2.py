@@ -416,9 +416,20 @@ class PagedBatch:
         self.ref = ctypes.byref(s)
 
 
+def _host_int32(a, name: str) -> np.ndarray:
+    a = np.asarray(a)
+    if a.size and a.dtype.kind not in "iu":
+        raise TypeError(f"{name} must hold integers, got {a.dtype}")
+    if a.size:
+        _int32(int(a.min()), name), _int32(int(a.max()), name)
+    return np.ascontiguousarray(a, dtype=np.int32)
+
+
 def paged_batch_check(q_start, kv_len, page_table, num_pages: int, page_size: int, rows: int) -> None:
-    """Checks a batch's lengths and page numbers on the host (arrays or CPU tensors)."""
-    host = [np.ascontiguousarray(a, dtype=np.int32) for a in (q_start, kv_len, page_table)]
+    """Checks a batch's lengths and page numbers on the host (integer arrays, lists or CPU tensors)."""
+    host = [_host_int32(a, n) for a, n in ((q_start, "q_start"), (kv_len, "kv_len"), (page_table, "page_table"))]
+    for v, n in ((num_pages, "num_pages"), (page_size, "page_size"), (rows, "rows")):
+        _int32(v, n)
     R = host[1].shape[0]
     if host[0].shape != (R + 1,) or host[2].ndim != 2 or host[2].shape[0] != R:
         raise ValueError("need q_start (R + 1), kv_len (R) and page_table (R, max_pages)")

@@ -146,3 +146,19 @@ def test_rows_per_batch_that_does_not_fit_32_bits(K2):
             K2.lora_linear(K2.KREA2_EPI_RESID, t(10, 64, dtype=bf), t(128, 64, dtype=bf), adapters,
                            t(4, dtype=torch.int32), t(3, dtype=torch.int32), t(10, 128), t(1 << 16, dtype=torch.uint8),
                            gate=t(1, 128), rows_per_batch=rows_per_batch)
+
+
+def test_batch_check_of_values_that_do_not_fit(K2):
+    # lengths, page numbers and sizes are refused, never cut to 32 bits or to whole numbers
+    big = 2 ** 32
+    for change in (dict(q_start=np.array([0, 3, 3, 8 + big])), dict(kv_len=torch.tensor([20, big, 5])),
+                   dict(kv_len=[20 - big, 0, 5]), dict(page_table=np.array([[4 + big, 1, -1], [-1] * 3, [2, 9, 7]])),
+                   dict(rows=10 + big), dict(num_pages=5 + big), dict(page_size=16 - big)):
+        with pytest.raises(ValueError, match="32 bits"):
+            K2.paged_batch_check(**{**GOOD, **change})
+    for change in (dict(kv_len=[20.9, 0, 5]), dict(q_start=torch.tensor([0.0, 3, 3, 8])),
+                   dict(page_table=[["4", "1", "2"]] * 3)):
+        with pytest.raises(TypeError):
+            K2.paged_batch_check(**{**GOOD, **change})
+    for dt in (np.int64, np.uint8, np.int32):  # other integer types of fitting values are fine
+        K2.paged_batch_check(**{**GOOD, "kv_len": np.array(GOOD["kv_len"], dtype=dt)})
