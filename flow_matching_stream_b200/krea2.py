@@ -403,6 +403,9 @@ class PagedBatch:
         _shape(page_table, (R, page_table.shape[1]), "page_table")
         if k_pages.dim() != 3 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
             raise ValueError("k_pages and v_pages must both be (num_pages, page_size, Hkv*D) of one dtype")
+        for v, n in ((R, "R"), (rows, "rows"), (page_table.shape[1], "max_pages"), (k_pages.shape[0], "num_pages"),
+                     (k_pages.shape[1], "page_size")):
+            _int32(v, n)
         self.dtype, self.device = k_pages.dtype, k_pages.device
         self.tensors = (q_start, kv_len, page_table, k_pages, v_pages)
         s = _lib.Krea2PagedBatch()
@@ -475,7 +478,7 @@ def gqa_attention_paged(dims, batch: PagedBatch, qkvg: torch.Tensor, q_norm_w: t
     table = (rows, D // 2)
     T, mask, end = 0, None, None
     if text_mask is not None:
-        T = text_mask.shape[-1]
+        T = _int32(text_mask.shape[-1], "text_mask's length")
         mask = _arg(text_mask, dev, torch.uint8, (batch.R, T), "text_mask")
     if key_end is not None:
         end = _arg(key_end, dev, torch.int32, (rows,), "key_end")
@@ -502,6 +505,8 @@ class LoraAdapters:
         _shape(up, (n, self.Nw, self.rank), "up")
         _want(scale, torch.float32, "scale")
         _shape(scale, (n,), "scale")
+        for v, m in ((n, "n_adapters"), (self.rank, "rank"), (self.K, "K"), (self.Nw, "Nw")):
+            _int32(v, m)
         self.down, self.up, self.scale = down, up, scale
         self.dtype, self.device = down.dtype, down.device
         if up.device != self.device or scale.device != self.device:
@@ -532,6 +537,8 @@ class LoraAdapters:
 
 
 def lora_workspace_size(dtype: torch.dtype, epilogue: int, M: int, Nw: int, K: int, R: int, rank: int) -> int:
+    for v, n in ((epilogue, "epilogue"), (M, "M"), (Nw, "Nw"), (K, "K"), (R, "R"), (rank, "rank")):
+        _int32(v, n)
     return int(lib().krea2_lora_workspace_size(dtype_code(dtype), epilogue, M, Nw, K, R, rank))
 
 
@@ -542,8 +549,9 @@ def lora_linear(epilogue: int, A: torch.Tensor, W: torch.Tensor, adapters: LoraA
 
     rows_per_batch = 0 gates a residual with the gate row of the row's request; gate_stride None is the
     gate's row length."""
-    dev, dt, K, Nw, R = adapters.dev, adapters.dtype, adapters.K, adapters.Nw, adapter.shape[0]
-    M = A.shape[0]
+    dev, dt, K, Nw, R = adapters.dev, adapters.dtype, adapters.K, adapters.Nw, _int32(adapter.shape[0], "R")
+    M = _int32(A.shape[0], "M")
+    _int32(epilogue, "epilogue")
     resid = epilogue == KREA2_EPI_RESID
     gate_p = None
     if resid:

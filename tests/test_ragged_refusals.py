@@ -162,3 +162,33 @@ def test_batch_check_of_values_that_do_not_fit(K2):
             K2.paged_batch_check(**{**GOOD, **change})
     for dt in (np.int64, np.uint8, np.int32):  # other integer types of fitting values are fine
         K2.paged_batch_check(**{**GOOD, "kv_len": np.array(GOOD["kv_len"], dtype=dt)})
+
+
+def test_binding_refuses_sizes_that_do_not_fit(K2):
+    import types
+
+    from flow_matching_stream_b200 import _lib
+    t, i32, big = torch.zeros, torch.int32, 2 ** 32
+    lengths = (t(3, dtype=i32), t(2, dtype=i32))
+    pages = (t(9, 16, 128), t(9, 16, 128))
+    with pytest.raises(ValueError, match="rows.*32 bits"):
+        K2.PagedBatch(*lengths, t(2, 4, dtype=i32), *pages, big + 10)
+    with pytest.raises(ValueError, match="max_pages.*32 bits"):
+        K2.PagedBatch(*lengths, t(2, 1, dtype=i32).expand(2, big + 4), *pages, 10)
+    batch = types.SimpleNamespace(dev=0, rows=10, R=2, kv_cols=KI.FULL.KVD, dtype=torch.float32)
+    with pytest.raises(ValueError, match="text_mask.*32 bits"):
+        K2.gqa_attention_paged(KI.FULL, batch, t(1), t(1), t(1), t(1), t(2, 1, dtype=torch.uint8).expand(2, big + 8),
+                               None, t(1), None)
+    sizes = dict(epilogue=0, M=10, Nw=256, K=128, R=2, rank=16)
+    assert K2.lora_workspace_size(torch.float32, **sizes) > 0
+    for name in sizes:
+        with pytest.raises(ValueError, match=f"{name}.*32 bits"):
+            K2.lora_workspace_size(torch.float32, **{**sizes, name: sizes[name] + big})
+    with pytest.raises(ValueError, match="K.*32 bits"):
+        K2.LoraAdapters(t(1, 1, 1).expand(2, 16, big + 64), t(2, 128, 16), t(2))
+    adapters = types.SimpleNamespace(dev=0, dtype=torch.float32, K=1, Nw=128, rank=16, struct=_lib.Krea2Lora())
+    call = (t(128, 1), adapters, t(3, dtype=i32), t(2, dtype=i32), t(1), t(1))
+    with pytest.raises(ValueError, match="M.*32 bits"):
+        K2.lora_linear(0, t(1, 1).expand(big + 1, 1), *call)
+    with pytest.raises(ValueError, match="epilogue.*32 bits"):
+        K2.lora_linear(big + 1, t(10, 1), *call)
