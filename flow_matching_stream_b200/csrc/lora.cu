@@ -169,16 +169,16 @@ int check_launch(const char* what) {
 int lora_simt(int epi, const LoraLinearArgs& a, const Krea2Lora& l, float* t, cudaStream_t stream) {
   const float* A = reinterpret_cast<const float*>(a.A);
   const float* W = reinterpret_cast<const float*>(a.W);
-  const long warps = (long)a.M * l.rank;
-  lora_down_simt_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(l, a.M, a.K, A, t);
-  int rc = check_launch("lora_down");
-  if (rc) return rc;
   // 64 x 128 tiles, or 16 x 32 where those would leave most SMs without one (73 x 640, K 256: 10 large tiles take
   // 55 us, 100 small ones 8 us; from two large tiles per SM on the large ones' reuse wins)
   const int groups = (a.N + 127) / 128;
   const bool small = (long long)groups * ((a.M + 63) / 64) < 2L * num_sms();
   const dim3 grid(small ? groups * 4 : groups, small ? (a.M + 15) / 16 : (a.M + 63) / 64);
   if (grid.y > 65535) return set_error(KREA2_ERR_UNSUPPORTED, "more than %d rows", 65535 * 64);
+  const long warps = (long)a.M * l.rank;
+  lora_down_simt_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(l, a.M, a.K, A, t);
+  int rc = check_launch("lora_down");
+  if (rc) return rc;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(small ? 128 : 256);

@@ -192,3 +192,15 @@ def test_binding_refuses_sizes_that_do_not_fit(K2):
         K2.lora_linear(0, t(1, 1).expand(big + 1, 1), *call)
     with pytest.raises(ValueError, match="epilogue.*32 bits"):
         K2.lora_linear(big + 1, t(10, 1), *call)
+
+
+def test_too_many_fp32_rows_are_refused_before_a_launch(K2):
+    from flow_matching_stream_b200 import _lib
+    lib, s = K2.lib(), _lib.Krea2Lora()
+    s.R, s.n_adapters, s.rank = 2, 1, 16
+    for k in ("row_start", "adapter", "scale", "down", "up"):
+        setattr(s, k, FAKE)
+    before = lib.krea2_launch_count()
+    assert lib.krea2_lora_linear(1, 0, 1 << 22, 2048, 64, FAKE, FAKE, ctypes.byref(s), FAKE, None, 0, 0, FAKE, 1 << 40,
+                                 None) == -5
+    assert lib.krea2_launch_count() == before
