@@ -218,3 +218,55 @@ def test_lora_fused_adapters_of_stacked_projections(K2):
         ref[a:b] += sc * torch.cat([(A[a:b].double() @ d.double().T) @ u.double().T for d, u in p], 1)
     rel, big = off(out, ref)
     assert rel <= TOL_BF16 and big <= 8 * TOL_BF16
+
+
+def sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+def one_tile_is_narrow(N):
+    # gemm_bf16_lora's choice between 64 and 128 columns for one row tile
+    def eff(tiles):
+        return tiles / (-(-tiles // sms()) * sms())
+    return eff(N // 64) > 1.25 * eff(N // 128)
+
+
+@pytest.mark.parametrize("epilogue", ["store", "resid"])
+@pytest.mark.parametrize("rows,spare,rank,K", [([1], 0, 16, 320), ([40, 0, 36, 1], 0, 64, 320), ([70, 7], 51, 24, 704),
+                                               ([128], 0, 256, 448), ([1] * 128, 0, 8, 64)])
+def test_lora_one_row_tile_in_128_columns(K2, epilogue, rows, spare, rank, K):
+    # K of an odd number of 64-column steps: a stage holds two, the last one is filled up with zeros
+    assert not one_tile_is_narrow(15360) and one_tile_is_narrow(768)
+    Case(K2, epilogue, rows, K, 15360, rank, 3, torch.bfloat16, ids=[0, -1, 2, 1][:len(rows)] if len(rows) < 5 else None,
+         spare=spare).check()
+
+
+@pytest.mark.parametrize("epilogue,N", [("store", 2048), ("store", 2010), ("resid", 2048), ("resid", 1999),
+                                        ("swiglu", 2048)])
+@pytest.mark.parametrize("rank", [8, 40])
+def test_lora_f32_large_tiles(K2, epilogue, N, rank):
+    # 64 x 128 tiles are taken from two per SM on; rows, columns and K end inside tiles
+    rows, K = [700, 0, 1, 599], 100
+    assert -(-N // 128) * -(-(sum(rows) + 9) // 64) >= 2 * sms()
+    Case(K2, epilogue, rows, K, N, rank, 3, torch.float32, ids=[2, 0, -1, 1], spare=9).check()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_lora_overlapping_calls(K2, dtype):
+    # two streams with calls in flight at once, each with its own workspace and outputs
+    cases = [Case(K2, "store", [1, 70, 200], 1024, 1536, 48, 3, dtype, seed=1),
+             Case(K2, "store", [33, 129], 512, 768, 16, 2, dtype, seed=2)]
+    want = [c.run() for c in cases]
+    turns = 20
+    outs = [[torch.empty_like(c.out0) for _ in range(turns)] for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for i in range(turns):
+        for k in ((0, 1), (1, 0))[i % 2]:
+            c = cases[k]
+            K2.lora_linear(c.epi, c.A, c.W, c.lora, c.row_start, c.adapter, outs[k][i], c.ws, stream=streams[k])
+    torch.cuda.synchronize()
+    K2.check_device_error()
+    for c, w, os in zip(cases, want, outs):
+        for o in os:
+            assert torch.equal(o[:c.used], w[:c.used])

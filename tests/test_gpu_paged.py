@@ -425,3 +425,35 @@ def test_page_numbers_outside_the_pool_are_reported(K2, page):
         K2.check_device_error()
     assert e.value.code == -1
     assert torch.equal(out[:3], want[:3])
+
+
+# ----------------------------------------------- batches of about one new token per request (16 query rows an item)
+
+@pytest.mark.parametrize("d", [dims(8, 2), dims(6, 3), dims(3, 3)], ids=["g4", "g2", "g1"])
+def test_attention_few_rows(K2, d):
+    b = Ragged(d, [1, 0, 2, 1, 3], [300, 50, 1700, 64, 5000], 16, torch.bfloat16, "cuda", spare=1)
+    assert b.rows <= 2 * b.R
+    b.poison()
+    g = torch.Generator().manual_seed(6)
+    end = torch.randint(-5, 6000, (b.rows,), generator=g, dtype=torch.int32).cuda()
+    for mask in (None, random_mask(b, 250, 0.4)):
+        for key_end in (None, end, causal(b)):
+            check_attention(K2, b, mask, key_end)
+
+
+def test_attention_one_long_chunk_among_empty_requests(K2):
+    # 16-row items by the row count, yet one request has all the rows: whole rounds of items and a rest
+    b = Ragged(dims(8, 2), [0] * 300 + [1400] + [0] * 420, [3] * 300 + [1500] + [0] * 420, 64, torch.bfloat16, "cuda",
+               spare=11)
+    assert b.rows <= 2 * b.R and 1400 // 4 * b.d.Hkv > 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    b.poison()
+    check_attention(K2, b)
+    check_attention(K2, b, key_end=causal(b))
+
+
+def test_attention_causal_prompts(K2):
+    # prompts read from nothing: most of an item's key tiles lie behind its tokens' key ends
+    for new in ([1500], [400, 1, 650, 64]):
+        b = Ragged(dims(8, 2), new, new, 64, torch.bfloat16, "cuda", spare=3)
+        b.poison()
+        check_attention(K2, b, key_end=causal(b))
