@@ -7,6 +7,8 @@
 // requests of 4096 new tokens over 8704 keys 1.69 to 1.80 ms by box, 970 to 1040 TFLOP/s under the power cap (71 to
 // 75 % of the sustained matrix rate), with tensor pipe, exponentials and issue slots each about half busy (a smaller
 // batch: 48, 52 and 53 %); eight single tokens over 521 to 8704 keys 50 to 53 us, 4.3 to 4.6 TB/s, the join 7 of them.
+// (These rates count all keys. Tiles that the text mask removes whole are neither loaded nor computed: in these
+// batches 3 to 5 % of the keys, up to 7.5 % by the drawn masks.)
 //
 // Roundings: q_hat and P go to the tensor cores in bf16, as K and V come; maxima, sums and O are fp32. Against fp64
 // the output is off by 0.0025 to 0.0029 of its size, where its own rounding to bf16 makes 0.0017. Carrying what those
@@ -22,6 +24,9 @@
 //   * an equal share of the key tiles of what is left, cut without regard to items. A cut item's parts
 //     (unnormalised O, row maximum and sum, fp32) go to the workspace, and a second kernel joins them in
 //     key order. One new token over a long cache is spread over all SMs this way.
+// An item weighs all tiles of its request, also where its tokens' key ends drop many of them, so shares of causal
+// prompts are unequal: 4096 tokens read from nothing take 315 us where all of them read all keys in 410, four of 1000
+// 162 and 176 (half the operations each).
 // Batches of about one new token per request have items of one team with 16 rows, two CTAs per SM.
 //
 // Roles as in attention_tc.cu, but the CTA runs through segments (an item or a part of one):
@@ -914,7 +919,11 @@ struct Shape {
 Shape shape_of(const Krea2PagedBatch& b, int H, int Hkv) {
   const int G = H / Hkv;
   Shape s;
-  // about one new token per request, or so few that an item of 16 rows holds them
+  // About one new token per request, or so few that an item of 16 rows holds them. 16 rows against 256 rows an item:
+  // eight single tokens over 521 to 8704 keys 49.9 and 52.7 us, 128 over 2048 keys 255 and 276, 128 of these beside a
+  // chunk of 128 over 8704 443 and 478. The host knows rows and requests only, not how the rows are spread: one chunk
+  // of 600 over 8704 keys beside 299 empty requests takes 793 us in 16-row items, 153 in the others. A batch that may
+  // hold such a chunk should have more than two rows per request (rows behind the last request are no work).
   s.few = b.M <= 2LL * b.R || b.M * (long long)G <= 16;
   const int rows = s.few ? 16 : 256, qpos = rows / G;
   const long long qtiles = b.M < b.M / qpos + b.R ? b.M : b.M / qpos + (long long)b.R;

@@ -703,7 +703,8 @@ int launch_gemm_bn(const GemmParams& p0, const void* A, const void* W, cudaStrea
 }
 
 // The GEMM with the adapters' K steps, launched as a programmatic dependent of lora_down: its CTAs
-// start as soon as every lora_down CTA runs, and wait for t only when they first load it. Bound by the tensor
+// may start once every lora_down CTA runs, and wait for t only when they first load it. A CTA takes nearly all of an
+// SM's shared memory, so it starts where lora_down's CTAs have left; with many rows that is near lora_down's end. Bound by the tensor
 // cores, under the power cap: gate/up of 5760 rows, rank 16, 1.82 to 1.87 ms by box with t's own kernel (90 to 93 % of
 // the sustained matrix rate). The shared projection alone takes 1.74 to 1.81 ms from run to run.
 template <int BN, int EPI, bool WIDE>
@@ -735,8 +736,11 @@ int launch_gemm_lora_bn(const GemmParams& p0, const void* A, const void* W, cons
     // One row tile streams W once, and a stage's turn (a wait, a load of A and one of W by one thread) takes
     // about 0.3 us whatever it loads: as many K steps a stage as leave three stages. One row by 6144 x 6144 with an
     // adapter: 30.9 us with one K step a stage (30.8 us for N = 1024 too), 22.9 with two, 21.2 with four. What is
-    // left is W's 128-byte operand columns: loads alone in that order reach 3.8 TB/s from HBM, in runs of 512 bytes
-    // a row, which the operand layout does not allow, 5.2 TB/s. A ring holds two steps of 128 rows at least.
+    // left (20.0 us of device time) is about 7.5 us of start, end and two launches, and 2.0 ns a column of K, a CTA's
+    // own 64 columns of W at 64 GB/s. That part goes by K, not by N, until the CTAs together reach the memory's rate:
+    // N = 1024 (16 CTAs) 18.3 us, N = 6144 (96 CTAs, 6.1 TB/s while they stream) 20.0, and with K of 1536 and 12288
+    // 10.4 and 32.0; N = 15360 in 128 columns 34.8. Without an adapter 0.4 us less. A ring holds two steps of 128
+    // rows at least.
     const int step = lt.a_pitch + Cfg::B_BYTES, ring = Cfg::STAGES * Cfg::STAGE_BYTES;
     lt.kch = 12 * step <= ring ? 4 : 2;
     lt.stage_bytes = lt.kch * step;

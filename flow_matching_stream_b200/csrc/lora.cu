@@ -3,7 +3,8 @@
 // then the epilogue of krea2_linear on y. This file has the dispatch and the fp32 path (SIMT, reference
 // precision); bf16 runs on the tensor cores (lora_tc.cu, gemm_tcgen05.cu). The low-rank product
 // t = scale A downᵀ is (rows, rank), so it goes through the workspace; its product with up is added in the
-// projection's accumulators.
+// projection's accumulators. The fp32 path at full width, rank 16: 512 rows by 15360 x 6144 4.3 ms, by 32768 x 6144
+// (SwiGLU) 8.4 ms, by 6144 x 16384 (residual) 4.8 ms, 21 to 25 TFLOP/s; one row by 6144 x 6144 172 us.
 #include <math.h>
 
 #include "krea2_device.cuh"

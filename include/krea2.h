@@ -122,8 +122,9 @@ typedef struct {
 const char* krea2_last_error_string(void);
 
 /* Synchronises `stream`, then reads and clears the device error word set by an expired
- * bounded wait. Returns KREA2_OK, KREA2_ERR_TIMEOUT or KREA2_ERR_CUDA. This is the only
- * entry point that synchronises. */
+ * bounded wait or by a kernel that found a ragged batch's device arrays inconsistent. Returns
+ * KREA2_OK, KREA2_ERR_TIMEOUT, KREA2_ERR_ARG (an inconsistent batch) or KREA2_ERR_CUDA. This is
+ * the only entry point that synchronises. */
 int krea2_check_device_error(void* stream);
 
 /* Self-test of the failure detection: launches one kernel that waits, with a limit of limit_ms
@@ -420,9 +421,11 @@ int krea2_backbone_forward(const Krea2Dims* dims, int B, int T, int N, int dtype
  *   page_size  a multiple of 16; max_pages * page_size <= 2^30
  *   k_pages, v_pages (num_pages, page_size, Hkv*D) in `dtype`, 16-byte aligned
  * A request whose lengths are inconsistent (q_start not ascending or beyond M, kv_len below its new
- * tokens or beyond max_pages * page_size) is skipped: its rows and pages stay as they were. A page
- * number outside [0, num_pages) is never accessed; output rows that needed it are unspecified. Both
- * set the device error word, which krea2_check_device_error reports as KREA2_ERR_ARG. */
+ * tokens or beyond max_pages * page_size) is skipped: its rows and pages stay as they were. Where
+ * q_start falls, two consistent requests may claim the same rows: those rows, and the new tokens'
+ * slots of these requests, are unspecified. A page number outside [0, num_pages) is never accessed;
+ * output rows that needed it are unspecified. All of these set the device error word, which
+ * krea2_check_device_error reports as KREA2_ERR_ARG. */
 enum { KREA2_MAX_REQUESTS = 4096 };
 typedef struct {
   int R, M;
@@ -463,7 +466,9 @@ int krea2_paged_kv_append(const Krea2Dims* dims, const Krea2PagedBatch* batch, i
  *   workspace: krea2_paged_attention_workspace_size bytes, 256-byte aligned (NULL allowed when that
  *     is 0). It needs no initial value; calls that may overlap on the GPU need one each.
  * Kernels: bf16 with D = 128 and H/Hkv in {1, 2, 4} runs on the tensor cores; other shapes and fp32
- * run a SIMT kernel (D in {64, 128}). */
+ * run a SIMT kernel (D in {64, 128}), which is for small batches. A tensor-core batch with M <= 2R is
+ * taken to have about one new token per request; one that may hold a long chunk among few others should
+ * have more rows than that (rows behind the last request are no work). */
 size_t krea2_paged_attention_workspace_size(const Krea2Dims* dims, const Krea2PagedBatch* batch, int dtype);
 int krea2_gqa_attention_paged(const Krea2Dims* dims, const Krea2PagedBatch* batch, int T, int dtype,
                               const void* qkvg, const float* q_norm_w, const float* cos, const float* sin,
@@ -500,7 +505,8 @@ typedef struct {
  * of mantissa (bf16) or in fp32.
  * KREA2_EPI_RESID: rows_per_batch > 0 takes the gate row r / rows_per_batch as krea2_linear does;
  * rows_per_batch = 0 takes the gate row of the row's request.
- * bf16 path: Nw % 128 == 0, K % 64 == 0; A, W, down, up and out 16-byte aligned.
+ * A, W, down, up and out 16-byte aligned; 1 <= R <= KREA2_MAX_REQUESTS, M <= 2^22 (fp32: 65535 tiles of
+ * 64 rows where the tiles are large), else KREA2_ERR_UNSUPPORTED. bf16 path: Nw % 128 == 0, K % 64 == 0.
  * workspace: krea2_lora_workspace_size bytes, 256-byte aligned; it needs no initial value, and calls
  * that may overlap on the GPU need one each. */
 size_t krea2_lora_workspace_size(int dtype, int epilogue, int M, int Nw, int K, int R, int rank);
